@@ -11,14 +11,15 @@
 #include <mutex>
 #include <new>
 
+#include "api_util.hpp"
 #include "gemm_diag.h"
 #include "internal.hpp"
 
 using namespace stg;
 
-namespace {
+namespace stg {
 
-thread_local char g_last_error[512] = "";
+static thread_local char g_last_error[512] = "";
 
 gemm_status_t fail(gemm_status_t st, const char *fmt, ...)
 {
@@ -39,6 +40,10 @@ gemm_status_t hip_fail(hipError_t e, const char *what)
 {
     return fail(GEMM_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+} // namespace stg
+
+namespace {
 
 bool is_fp8(int t) { return t == GEMM_F8_E4M3 || t == GEMM_F8_E5M2; }
 // MX element formats: their bits and the scaled MFMA's format selector
@@ -117,12 +122,6 @@ int out_kind(int d)
     }
 }
 
-// a * b for a, b >= 0, saturating at INT64_MAX (size checks never overflow)
-int64_t smul(int64_t a, int64_t b)
-{
-    return (a != 0 && b > INT64_MAX / a) ? INT64_MAX : a * b;
-}
-
 // Fill packed leading dimensions; returns false if a given one is too small.
 bool normalise(gemm_desc_t &d)
 {
@@ -136,14 +135,12 @@ bool normalise(gemm_desc_t &d)
     return fix(d.lda, a_min) & fix(d.ldb, b_min) & fix(d.ldc, d.N) & fix(d.ldd, d.N);
 }
 
-struct DeviceInfo {
-    int checked = 0;
-    int is_gfx950 = 0;
-    int num_cu = 0;
-    char arch[64] = "";
-};
 DeviceInfo g_dev[64];
 std::mutex g_dev_mu;
+
+} // namespace
+
+namespace stg {
 
 gemm_status_t check_device(int *dev_out, DeviceInfo *info_out)
 {
@@ -174,6 +171,10 @@ gemm_status_t check_device(int *dev_out, DeviceInfo *info_out)
     return GEMM_OK;
 }
 
+} // namespace stg
+
+namespace {
+
 // Can the LDS-tiled kernel serve this descriptor (ignoring pointer alignment)?
 bool tiled_ok(const gemm_desc_t &d)
 {
@@ -192,10 +193,6 @@ bool tiled_ok(const gemm_desc_t &d)
     return d.K > 0 && (d.K * eb) % 64 == 0 && (d.lda * eb) % 16 == 0 && (d.ldb * eb) % 16 == 0 &&
            a_ok && b_ok;
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 const char *family_name(int f)
 {
@@ -667,22 +664,6 @@ gemm_status_t gemm_plan_describe(const gemm_plan_t *plan, char *buf, size_t len)
     snprintf(buf, len, "%s", plan->name);
     return ok();
 }
-
-// Byte range [lo, hi) of a matrix of `rows` rows of `cols` elements of
-// `eb` bytes, `ld` elements apart.
-struct Span {
-    uintptr_t lo = 0, hi = 0;
-};
-static Span span(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t eb)
-{
-    Span s;
-    if (!p || rows <= 0 || cols <= 0)
-        return s;
-    s.lo = (uintptr_t)p;
-    s.hi = s.lo + (uintptr_t)(((rows - 1) * ld + cols) * eb);
-    return s;
-}
-static bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 
 // D must not share bytes with any input, except that D may be C itself
 // (in-place accumulate: same address, element size and leading dimension,

@@ -1,4 +1,4 @@
-"""Python binding of libstgemm.so (include/gemm.h).  Argument marshalling only:
+"""Python binding of libstgemm.so (include/gemm.h, include/gemm_moe.h).  Argument marshalling only:
 every step of the computation runs in the library's HIP kernels.  Device
 buffers are passed as torch tensors (their data pointers) or raw integer
 addresses; PyTorch provides memory and streams only.
@@ -6,7 +6,10 @@ addresses; PyTorch provides memory and streams only.
 The functions carry the C names: gemm_validate_desc, gemm_plan,
 gemm_plan_destroy, gemm_plan_describe, gemm_run, gemm_sparse24_sizes,
 gemm_sparse24_compress, gemm_sparse24_compress_noalloc, gemm_sparse24_run, gemm_mx_run, gemm_w4a16_run, gemm_status_string,
-gemm_last_error.  Non-OK statuses raise GemmError (except
+gemm_last_error, and from gemm_moe.h gemm_moe_sort_workspace,
+gemm_moe_sort, gemm_moe_dispatch, gemm_moe_combine, gemm_moe_combine_backward,
+gemm_grouped_validate_desc, gemm_grouped_plan, gemm_grouped_run,
+gemm_q8_store, gemm_q8_load, gemm_swiglu, gemm_swiglu_backward.  Non-OK statuses raise GemmError (except
 gemm_validate_desc, which returns the status).
 """
 import ctypes
@@ -30,6 +33,8 @@ DTYPES = {"f16": 1, "bf16": 2, "e4m3": 3, "e5m2": 4, "s8": 5, "f32": 6, "s32": 7
           "e2m3": 8, "e3m2": 9, "e2m1": 10, "u4": 11, "u8": 12}
 ROW_MAJOR, COL_MAJOR = 0, 1
 ACT_NONE, ACT_RELU = 0, 1
+# gemm_grouped_mode_t
+GROUPED = {"rows": 0, "weights": 1}
 # gemm_algo_t
 ALGO = {"auto": 0, "tiled": 1, "generic": 2, "skinny": 3, "tiled128": 4, "tiled256": 5}
 
@@ -57,6 +62,16 @@ class gemm_desc_t(ctypes.Structure):
     ]
 
 
+class gemm_grouped_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("mode", ctypes.c_int32), ("groups", ctypes.c_int32),
+        ("rows", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("a_type", ctypes.c_int32), ("b_type", ctypes.c_int32), ("d_type", ctypes.c_int32),
+        ("b_layout", ctypes.c_int32), ("has_c", ctypes.c_int32), ("algo", ctypes.c_int32),
+        ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64), ("ldd", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -72,6 +87,8 @@ def load():
     vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
     st = ctypes.c_int
     dp = ctypes.POINTER(gemm_desc_t)
+    gdp = ctypes.POINTER(gemm_grouped_desc_t)
+    sz = ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "gemm_validate_desc": (st, [dp]),
         "gemm_plan": (st, [dp, ctypes.POINTER(vp)]),
@@ -85,6 +102,22 @@ def load():
         "gemm_sparse24_compress": (st, [i64, i64, i32, vp, vp, vp, vp]),
         "gemm_sparse24_compress_noalloc": (st, [i64, i64, i32, vp, vp, vp, vp]),
         "gemm_sparse24_run": (st, [vp, vp, vp, vp, vp, vp, vp, vp]),
+        "gemm_moe_sort_workspace": (st, [i64, i64, i64, sz]),
+        "gemm_moe_sort": (st, [i64, i64, i64, i32, vp, vp, vp, vp, vp, vp]),
+        "gemm_moe_dispatch": (st, [i64, i64, i64, i64, i32, i32, vp, vp, i64, vp, vp, vp, vp, i64,
+                                   vp, vp]),
+        "gemm_moe_combine": (st, [i64, i64, i64, i32, vp, vp, vp, i64, i64, vp, i64, vp]),
+        "gemm_moe_combine_backward": (st, [i64, i64, i64, i32, vp, vp, vp, i64, vp, i64, i64, vp,
+                                           i64, vp, vp]),
+        "gemm_grouped_validate_desc": (st, [gdp]),
+        "gemm_grouped_plan": (st, [gdp, ctypes.POINTER(vp)]),
+        "gemm_grouped_plan_destroy": (st, [vp]),
+        "gemm_grouped_plan_describe": (st, [vp, ctypes.c_char_p, ctypes.c_size_t]),
+        "gemm_grouped_run": (st, [vp, vp, vp, vp, vp, vp, vp, vp]),
+        "gemm_q8_store": (st, [i64, i64, i32, vp, i64, vp, vp, vp]),
+        "gemm_q8_load": (st, [i64, i64, i32, vp, vp, vp, i64, vp]),
+        "gemm_swiglu": (st, [i64, i64, i32, vp, i64, vp, i64, vp, vp, vp]),
+        "gemm_swiglu_backward": (st, [i64, i64, i32, vp, vp, vp, i64, vp, i64, vp, i64, vp]),
         "gemm_diag_mfma_loop": (st, [i32, i32, i64, vp, vp]),
         "gemm_status_string": (ctypes.c_char_p, [st]),
         "gemm_last_error": (ctypes.c_char_p, []),
@@ -237,6 +270,122 @@ def gemm_mx_run(plan, A, scale_a, B, scale_b, C, bias, D, stream=None):
 def gemm_w4a16_run(plan, A, B, scales, zeros, C, bias, D, stream=None):
     _check(load().gemm_w4a16_run(plan.handle, _ptr(A), _ptr(B), _ptr(scales), _ptr(zeros),
                                  _ptr(C), _ptr(bias), _ptr(D), _stream(stream)))
+
+
+# ---------------------------------------------------------------- gemm_moe.h
+# Argument order is the C functions'; a leading dimension of 0 means packed.
+
+def gemm_moe_sort_workspace(tokens, topk, groups):
+    """Bytes of workspace of gemm_moe_sort and gemm_moe_dispatch."""
+    n = ctypes.c_size_t()
+    _check(load().gemm_moe_sort_workspace(tokens, topk, groups, ctypes.byref(n)))
+    return n.value
+
+
+def gemm_moe_sort(tokens, topk, groups, ids, offsets, order, pos, workspace, id_bytes=4,
+                  stream=None):
+    _check(load().gemm_moe_sort(tokens, topk, groups, id_bytes, _ptr(ids), _ptr(offsets),
+                                _ptr(order), _ptr(pos), _ptr(workspace), _stream(stream)))
+
+
+def gemm_moe_dispatch(tokens, topk, groups, cols, dtype, ids, X, ldx, offsets, order, pos, Xs,
+                      ldxs, workspace, id_bytes=4, stream=None):
+    _check(load().gemm_moe_dispatch(tokens, topk, groups, cols, DTYPES[dtype], id_bytes, _ptr(ids),
+                                    _ptr(X), ldx, _ptr(offsets), _ptr(order), _ptr(pos), _ptr(Xs),
+                                    ldxs, _ptr(workspace), _stream(stream)))
+
+
+def gemm_moe_combine(tokens, topk, cols, dtype, pos, weights, Ys, ldys, rows, Y, ldy, stream=None):
+    _check(load().gemm_moe_combine(tokens, topk, cols, DTYPES[dtype], _ptr(pos), _ptr(weights),
+                                   _ptr(Ys), ldys, rows, _ptr(Y), ldy, _stream(stream)))
+
+
+def gemm_moe_combine_backward(tokens, topk, cols, dtype, pos, weights, dY, lddy, Ys, ldys, rows,
+                              dYs, lddys, dw, stream=None):
+    _check(load().gemm_moe_combine_backward(tokens, topk, cols, DTYPES[dtype], _ptr(pos),
+                                            _ptr(weights), _ptr(dY), lddy, _ptr(Ys), ldys, rows,
+                                            _ptr(dYs), lddys, _ptr(dw), _stream(stream)))
+
+
+def make_grouped_desc(mode, rows, N, K, groups, a_type, b_type, d_type, *, b_layout=None,
+                      has_c=False, lda=0, ldb=0, ldd=0, algo="auto"):
+    """Build a gemm_grouped_desc_t; mode "rows" (D[r] = A[r] B_g, B_g N x K
+    for b_layout "col", the default there, K x N for "row") or "weights"
+    (D_g = A_g^T B_g (+ C_g), K x N)."""
+    d = gemm_grouped_desc_t()
+    d.mode, d.groups = GROUPED[mode], groups
+    d.rows, d.N, d.K = rows, N, K
+    d.a_type, d.b_type, d.d_type = DTYPES[a_type], DTYPES[b_type], DTYPES[d_type]
+    if b_layout is None:
+        b_layout = "col" if mode == "rows" else "row"
+    d.b_layout = ROW_MAJOR if b_layout == "row" else COL_MAJOR
+    d.has_c = int(bool(has_c))
+    d.algo = ALGO[algo] if isinstance(algo, str) else int(algo)
+    d.lda, d.ldb, d.ldd = lda, ldb, ldd
+    return d
+
+
+def gemm_grouped_validate_desc(desc):
+    """Returns the status code (GEMM_OK or an error); never raises."""
+    return load().gemm_grouped_validate_desc(ctypes.byref(desc) if desc is not None else None)
+
+
+class GroupedPlan:
+    """Owns a gemm_grouped_plan_t*; released by close()."""
+
+    def __init__(self, handle, desc):
+        self.handle = handle
+        self.desc = desc
+
+    def close(self):
+        if self.handle:
+            load().gemm_grouped_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def name(self):
+        buf = ctypes.create_string_buffer(128)
+        _check(load().gemm_grouped_plan_describe(self.handle, buf, len(buf)))
+        return buf.value.decode()
+
+
+def gemm_grouped_plan(desc):
+    h = ctypes.c_void_p()
+    _check(load().gemm_grouped_plan(ctypes.byref(desc), ctypes.byref(h)))
+    return GroupedPlan(h.value, desc)
+
+
+def gemm_grouped_run(plan, A, B, scales, offsets, C, D, stream=None):
+    _check(load().gemm_grouped_run(plan.handle, _ptr(A), _ptr(B), _ptr(scales), _ptr(offsets),
+                                   _ptr(C), _ptr(D), _stream(stream)))
+
+
+def gemm_q8_store(rows, cols, dtype, X, ldx, codes, scales, stream=None):
+    _check(load().gemm_q8_store(rows, cols, DTYPES[dtype], _ptr(X), ldx, _ptr(codes), _ptr(scales),
+                                _stream(stream)))
+
+
+def gemm_q8_load(rows, cols, dtype, codes, scales, X, ldx, stream=None):
+    _check(load().gemm_q8_load(rows, cols, DTYPES[dtype], _ptr(codes), _ptr(scales), _ptr(X), ldx,
+                               _stream(stream)))
+
+
+def gemm_swiglu(rows, cols, dtype, GU, ldgu, H, ldh, codes=None, scales=None, stream=None):
+    _check(load().gemm_swiglu(rows, cols, DTYPES[dtype], _ptr(GU), ldgu, _ptr(H), ldh, _ptr(codes),
+                              _ptr(scales), _stream(stream)))
+
+
+def gemm_swiglu_backward(rows, cols, dtype, codes, scales, dH, lddh, dGU, lddgu, H=None, ldh=0,
+                         stream=None):
+    _check(load().gemm_swiglu_backward(rows, cols, DTYPES[dtype], _ptr(codes), _ptr(scales),
+                                       _ptr(dH), lddh, _ptr(dGU), lddgu, _ptr(H), ldh,
+                                       _stream(stream)))
 
 
 def gemm_diag_mfma_loop(kind, blocks, iters, out, stream=None):

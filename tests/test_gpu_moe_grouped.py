@@ -1,0 +1,231 @@
+"""Grouped products (gemm_grouped_run) on the GPU against plain 64-bit
+products, group by group, for every kernel family that takes the sizes."""
+import pytest
+import torch
+
+import moe_ref as R
+from gpu_util import say
+from sparse_tiled_gemm_amd import gemm as G
+
+pytestmark = pytest.mark.gpu
+
+FAMILIES = ["auto", "generic", "skinny", "tiled128", "tiled256"]
+
+
+def _plan(algo, *a, **kw):
+    """A plan, or a skip where the forced family does not take the sizes."""
+    try:
+        return G.gemm_grouped_plan(G.make_grouped_desc(*a, algo=algo, **kw))
+    except G.GemmError as e:
+        if algo != "auto" and e.status == G.GEMM_ERR_UNSUPPORTED:
+            pytest.skip("%s does not take these sizes" % algo)
+        raise
+
+
+def _mat(gen, rows, cols, dtype, ld=0, scale=1.0, off=0):
+    ld = ld or cols
+    buf = torch.full((rows * ld + 64,), float("nan"), dtype=R.DT[dtype], device="cuda")
+    v = buf[off:off + rows * ld].view(rows, ld)
+    v[:, :cols] = (torch.randn(rows, cols, generator=gen) * scale).to(R.DT[dtype])
+    return v[:, :cols], buf
+
+
+def _bounds(counts, lead=0):
+    o = [lead]
+    for c in counts:
+        o.append(o[-1] + c)
+    return o
+
+
+# rows outside every group (before the first, after the last), empty groups,
+# groups of one row, groups that end inside a tile
+ROWS = [  # counts, lead, tail, N, K, dtype, d_type, ld extra, element offset
+    ([1], 0, 0, 64, 64, "bf16", "bf16", 0, 0),
+    ([0, 1, 0, 3], 0, 0, 1024, 2048, "bf16", "bf16", 0, 0),
+    ([1, 1, 1, 1, 0], 0, 0, 96, 256, "f16", "f16", 0, 0),
+    ([5, 0, 17, 16, 40, 0, 1], 2, 3, 200, 136, "f16", "f32", 0, 0),
+    ([130, 0, 64, 300], 0, 0, 264, 1416, "bf16", "bf16", 8, 0),
+    ([257, 256, 0, 1, 500], 1, 9, 520, 72, "f16", "f16", 0, 0),
+    ([40, 25], 0, 0, 33, 45, "bf16", "f32", 3, 1),       # nothing aligned
+    ([70, 3], 0, 0, 128, 8, "bf16", "bf16", 0, 0),
+    ([3] * 70, 0, 0, 64, 128, "bf16", "bf16", 0, 0),     # more groups than lanes
+    ([0, 0], 0, 5, 64, 64, "f16", "f16", 0, 0),
+    ([33, 600], 0, 0, 776, 1032, "f16", "f32", 0, 0),
+    ([4, 9], 0, 0, 64, 0, "bf16", "f32", 0, 0),          # an empty sum
+]
+
+
+@pytest.mark.parametrize("algo", FAMILIES)
+@pytest.mark.parametrize("b_layout", ["col", "row"])
+@pytest.mark.parametrize("case", ROWS)
+def test_rows(case, b_layout, algo):
+    counts, lead, tail, N, K, dtype, d_type, ldx, off = case
+    say("rows", algo, b_layout, case)
+    gen = torch.Generator().manual_seed(N + K)
+    g = len(counts)
+    offsets = _bounds(counts, lead)
+    rows = offsets[-1] + tail
+    bw, bh = (K, N) if b_layout == "col" else (N, K)
+    plan = _plan(algo, "rows", rows, N, K, g, dtype, dtype, d_type, b_layout=b_layout,
+                 lda=K + ldx, ldb=bw + ldx, ldd=N + ldx)
+    A, _ = _mat(gen, rows, K, dtype, K + ldx, 1.0, off)
+    B, _ = _mat(gen, g * bh, bw, dtype, bw + ldx, max(K, 1) ** -0.5, off)
+    D, d_buf = _mat(gen, rows, N, d_type, N + ldx, 1.0, off)
+    before = d_buf.clone()
+    off_d = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    G.gemm_grouped_run(plan, A, B, None, off_d, None, D)
+    torch.cuda.synchronize()
+    got = D.cpu().double()
+    refs = R.rows_ref(A.cpu(), B.cpu().reshape(g, bh, bw), offsets, b_layout)
+    want = before.clone()
+    wv = want[off:off + rows * (N + ldx)].view(rows, N + ldx)
+    for a, ref, S in refs.values():
+        n = len(ref)
+        bound = R.half_step(d_type, ref) * 1.001 + (K + 2) * 2 * R.U32 * S
+        assert ((got[a:a + n] - ref).abs() <= bound).all(), plan.name
+        wv[a:a + n, :N] = D[a:a + n]
+    it = torch.int32 if d_type == "f32" else torch.int16
+    assert torch.equal(d_buf.view(it), want.view(it))  # nothing else is written
+
+
+@pytest.mark.parametrize("offsets", [[0, 40, 20, 60], [-7, 10, 1000, 64], [64, 64, 64, 0],
+                                     [2 ** 31 - 1, -2 ** 31, 30, 2 ** 31 - 1]])
+@pytest.mark.parametrize("algo", FAMILIES)
+@pytest.mark.parametrize("mode", ["rows", "weights"])
+def test_bounds_are_clamped(mode, offsets, algo):
+    """Bounds outside 0 .. rows or descending: clamped, empty, never out of range."""
+    gen = torch.Generator().manual_seed(1)
+    rows, N, K = 64, 64, 128
+    A, _ = _mat(gen, rows, K, "bf16")
+    off_d = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    if mode == "rows":
+        plan = _plan(algo, mode, rows, N, K, 3, "bf16", "bf16", "f32")
+        B, _ = _mat(gen, 3 * N, K, "bf16", 0, K ** -0.5)
+        D = torch.full((rows, N), 7.0, device="cuda")
+        G.gemm_grouped_run(plan, A, B, None, off_d, None, D)
+        torch.cuda.synchronize()
+        got = D.cpu().double()
+        refs = R.rows_ref(A.cpu(), B.cpu().reshape(3, N, K), offsets, "col")
+        hit = torch.zeros(rows, dtype=torch.int32)
+        for a, ref, _ in refs.values():
+            hit[a:a + len(ref)] += 1
+        for a, ref, S in refs.values():
+            sel = hit[a:a + len(ref)] == 1  # rows of two groups hold either's product
+            err = (got[a:a + len(ref)] - ref).abs()
+            assert (err[sel] <= (K + 2) * 2 * R.U32 * S[sel] + R.half_step("f32", ref)[sel]).all()
+        assert (got[hit == 0] == 7).all()
+    else:
+        plan = _plan(algo, mode, rows, N, K, 3, "bf16", "bf16", "f32")
+        B, _ = _mat(gen, rows, N, "bf16")
+        D = torch.empty(3, K, N, device="cuda")
+        G.gemm_grouped_run(plan, A, B, None, off_d, None, D)
+        torch.cuda.synchronize()
+        ref, S = R.weights_ref(A.cpu(), B.cpu(), offsets)
+        assert ((D.cpu().double() - ref).abs() <= (rows + 2) * 2 * R.U32 * S +
+                R.half_step("f32", ref)).all()
+
+
+WEIGHTS = [  # counts, lead, tail, K, N, dtype, d_type, C, eight, ld extra, element offset
+    ([1], 0, 0, 64, 64, "bf16", "f32", False, False, 0, 0),
+    ([0, 3, 0, 33], 0, 0, 128, 256, "bf16", "f32", True, False, 0, 0),
+    ([100, 0, 31, 200], 5, 2, 264, 136, "f16", "f32", False, False, 8, 0),
+    ([7, 64, 65], 0, 0, 300, 45, "f16", "bf16", True, False, 3, 1),     # nothing aligned
+    ([513, 40], 0, 0, 520, 776, "bf16", "f32", True, False, 0, 0),
+    ([96, 32], 0, 0, 256, 256, "f16", "f16", False, False, 0, 0),
+    ([0, 3, 0, 33], 0, 0, 128, 256, "bf16", "f32", True, True, 0, 0),
+    ([300, 0, 75], 1, 1, 264, 424, "f16", "f32", False, True, 0, 0),
+    ([90, 20], 0, 0, 72, 45, "bf16", "f32", False, True, 0, 0),
+    ([257, 255], 0, 0, 512, 512, "bf16", "bf16", True, True, 0, 0),
+    ([2] * 66, 0, 0, 64, 64, "bf16", "f32", False, False, 0, 0),
+]
+
+
+@pytest.mark.parametrize("algo", FAMILIES)
+@pytest.mark.parametrize("case", WEIGHTS)
+def test_weights(case, algo):
+    counts, lead, tail, K, N, dtype, d_type, has_c, eight, ldx, off = case
+    say("weights", algo, case)
+    gen = torch.Generator().manual_seed(N + K)
+    g = len(counts)
+    offsets = _bounds(counts, lead)
+    rows = offsets[-1] + tail
+    plan = _plan(algo, "weights", rows, N, K, g, dtype, "e4m3" if eight else dtype, d_type,
+                 has_c=has_c, lda=K + ldx, ldb=0 if eight else N + ldx, ldd=N + ldx)
+    A, _ = _mat(gen, rows, K, dtype, K + ldx, 1.0, off)
+    Bf, _ = _mat(gen, rows, N, dtype, N + ldx, 1.0, off)
+    B, scales, Bv = Bf, None, Bf.cpu()
+    if eight:
+        B = torch.empty(rows, N, dtype=torch.uint8, device="cuda")
+        scales = torch.empty(rows, (N + 31) // 32, dtype=torch.uint8, device="cuda")
+        G.gemm_q8_store(rows, N, dtype, Bf, N + ldx, B, scales)
+        torch.cuda.synchronize()
+        Bv = R.q8_load_ref(B.cpu(), scales.cpu(), dtype)
+    D, d_buf = _mat(gen, g * K, N, d_type, N + ldx, 1.0, off)
+    C, _ = _mat(gen, g * K, N, d_type, N + ldx, 1.0, off)
+    before = d_buf.clone()
+    off_d = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    G.gemm_grouped_run(plan, A, B, scales, off_d, C if has_c else None, D)
+    torch.cuda.synchronize()
+    c64 = C.cpu().reshape(g, K, N) if has_c else None
+    ref, S = R.weights_ref(A.cpu(), Bv, offsets, c64)
+    L = max(counts) + 2
+    bound = R.half_step(d_type, ref) * 1.001 + L * 2 * R.U32 * S
+    assert ((D.cpu().double().reshape(g, K, N) - ref).abs() <= bound).all(), plan.name
+    want = before.clone()
+    want[off:off + g * K * (N + ldx)].view(g * K, N + ldx)[:, :N] = D
+    it = torch.int32 if d_type == "f32" else torch.int16
+    assert torch.equal(d_buf.view(it), want.view(it))
+    if has_c:  # in place: the same bits
+        E, _ = _mat(gen, g * K, N, d_type, N + ldx, 1.0, off)
+        E.copy_(C)
+        G.gemm_grouped_run(plan, A, B, scales, off_d, E, E)
+        torch.cuda.synchronize()
+        assert torch.equal(E, D)
+
+
+@pytest.mark.parametrize("algo", FAMILIES)
+def test_rows_of_other_groups_do_not_leak(algo):
+    """NaN and infinity in one group's rows, in its weights and past K stay there."""
+    gen = torch.Generator().manual_seed(4)
+    N, K, lda = 72, 104, 112
+    offsets = [0, 20, 41, 75]
+    plan = _plan(algo, "rows", 75, N, K, 3, "bf16", "bf16", "f32", lda=lda, ldb=lda)
+    A, _ = _mat(gen, 75, K, "bf16", lda)   # NaN past K
+    B, _ = _mat(gen, 3 * N, K, "bf16", lda, K ** -0.5)
+    A[25] = float("nan")
+    A[30, 7] = float("inf")
+    B[N + 5] = float("nan")
+    D = torch.empty(75, N, device="cuda")
+    G.gemm_grouped_run(plan, A, B, None, torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+                       None, D)
+    torch.cuda.synchronize()
+    d = D.cpu()
+    assert torch.isfinite(d[:20]).all() and torch.isfinite(d[41:]).all()
+    assert torch.isnan(d[25]).all() and torch.isnan(d[20:41, 5]).all()
+    ok = [r for r in range(20, 41) if r not in (25, 30)]
+    assert torch.isfinite(d[ok][:, [c for c in range(N) if c != 5]]).all()
+
+
+@pytest.mark.parametrize("algo", FAMILIES)
+@pytest.mark.parametrize("eight", [False, True])
+def test_weights_of_other_groups_do_not_leak(algo, eight):
+    gen = torch.Generator().manual_seed(4)
+    N, K = 136, 72
+    offsets = [0, 20, 41, 75]
+    plan = _plan(algo, "weights", 80, N, K, 3, "f16", "e4m3" if eight else "f16", "f32")
+    A, _ = _mat(gen, 80, K, "f16")
+    Bf, _ = _mat(gen, 80, N, "f16")
+    A[25] = float("nan")
+    Bf[26, 3] = float("inf")
+    A[77], Bf[78] = float("nan"), float("nan")  # rows of no group
+    B, scales = Bf, None
+    if eight:
+        B = torch.empty(80, N, dtype=torch.uint8, device="cuda")
+        scales = torch.empty(80, (N + 31) // 32, dtype=torch.uint8, device="cuda")
+        G.gemm_q8_store(80, N, "f16", Bf, 0, B, scales)
+    D = torch.empty(3, K, N, device="cuda")
+    G.gemm_grouped_run(plan, A, B, scales, torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+                       None, D)
+    torch.cuda.synchronize()
+    d = D.cpu()
+    assert torch.isfinite(d[0]).all() and torch.isfinite(d[2]).all() and torch.isnan(d[1]).all()
