@@ -1,0 +1,478 @@
+// The LDS-tiled grouped product (gemm_moe.h, "grouped products") for 16-bit
+// operands on the 16x16x32 MFMA forms: k_grouped_tiled.
+//
+// A workgroup of eight waves owns a BM x BN tile of one group's output; a
+// wave owns a (BM/2) x (BN/4) block of it.  K advances 64 values a tile.
+// Both operands go from global memory straight into LDS (16 bytes per lane);
+// an operand of a K tile is kept as two regions, the first and the second
+// half of every wave's rows (columns), in two buffers, so a K tile is four
+// clusters of work, one per quadrant of the wave's block:
+//     cluster 0: read A0          MFMA A0 x B0
+//     cluster 1: read B1          MFMA A0 x B1
+//     cluster 2: read A1          MFMA A1 x B0
+//     cluster 3: read the next tile's B0, MFMA A1 x B1
+// Each cluster is a memory phase (LDS reads, copies for later) and an MFMA
+// phase with a barrier after each.  Waves 0-3 and waves 4-7 -- one of each
+// on every SIMD -- run one phase apart, so while one half multiplies the
+// other reads, and the matrix pipe is always fed by one of them.
+//
+// Copies: region R of tile t is read first in cluster n (n = 4t - 1, 4t, 4t
+// + 1, 4t + 2 for B0, A0, B1, A1) and is copied in the memory phase of
+// cluster n - 6.  With phases counted by barriers, the leading half's
+// cluster n reads in phase 2n and the trailing half's in 2n + 1.  What
+// cluster n read is in registers by the end of phase 2n + 2 (each MFMA
+// phase starts with lgkmcnt(0)), and its place is written again from cluster
+// n + 2 on, phase 2n + 4 at the earliest.  A wave waits for its copies of
+// cluster n - 6 at the end of its memory phase of cluster n - 1, phase 2n - 1
+// at the latest; the barrier there makes them visible to the reads of phase
+// 2n and later.
+//
+// Operand layouts in LDS (both without padding, as the copies need):
+//  - K-contiguous (rows of 64 K values = 8 chunks of 16 bytes): chunk c of
+//    region row r at slot c ^ (r & 7); a fragment read takes 16 rows at the
+//    chunks of four lane groups.
+//  - MN-major (64 K rows of the region's columns): 32-byte piece p of K row k
+//    at piece p ^ mn_swz(k), chosen so that the eight K rows half a wave
+//    touches in one transposing read lie on all eight pieces of a 256-byte
+//    window.
+// The permutation is applied to the lanes' global addresses.
+//
+// An 8-bit B (codes and scales of a checkpoint) is loaded into registers
+// instead, and brought to 16 bits and stored to LDS four clusters later.
+#pragma once
+#include "grouped_common.hpp"
+
+namespace stg {
+
+enum { GL_K = 0, GL_MN = 1, GL_Q8 = 2 }; // operand layouts: K-contiguous, MN-major, 8-bit MN-major
+
+// Workgroup id -> tile of `total`, a contiguous run of tiles per XCD (ids go
+// round robin over the 8 XCDs); -1 past the end.
+__device__ STG_AI inline int xcd_tile(int id, int total)
+{
+    const int per = (total + 7) >> 3, slot = id >> 3, t = (id & 7) * per + slot;
+    return slot < per && t < total ? t : -1;
+}
+
+// Tile `t` of tm x tn ones in groups of 8 tile rows walked column by column.
+__device__ STG_AI inline void tile_of(int t, int tiles_m, int tiles_n, int &tm, int &tn)
+{
+    const int per_group = 8 * tiles_n, group = t / per_group, first = group * 8;
+    const int rows = min(tiles_m - first, 8), in = t - group * per_group;
+    tm = first + in % rows;
+    tn = in / rows;
+}
+
+// Row tiles of all groups.
+template <int BM>
+__device__ STG_AI inline int count_tiles(const GroupedArgs &a, int lane)
+{
+    int n = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += 64)
+        if (g0 + lane < a.groups) {
+            int b, e;
+            group_bounds(a, g0 + lane, b, e);
+            n += (e - b + BM - 1) / BM;
+        }
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+        n += __shfl_xor(n, d);
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
+// One operand of the tile: where its rows (columns) lie and how it moves.
+// LAYOUT: GL_*; R: rows (columns) of a region; PIECE: rows of one wave in it
+// (region row i is tile row (i / PIECE) * 2 PIECE + half * PIECE + i % PIECE).
+template <int LAYOUT, int R, int PIECE, bool BF>
+struct Operand {
+    static constexpr bool KC = LAYOUT == GL_K;
+    static constexpr int LD = R * 128 / 8192;       // 1 KB copies per wave and region
+    static constexpr int VM = LAYOUT == GL_Q8 ? 2 * LD : LD; // vector-memory instructions
+    static constexpr int PITCH = R * 2;             // MN-major: bytes of a K row
+    static constexpr int CPR = PITCH / 16;          // its 16-byte chunks
+    static constexpr int FR = PIECE / 16;           // fragments of a wave
+    static_assert(LD >= 1, "a region is at least one copy per wave");
+
+    // (a transposing read touches K rows 8 q + 4 t + 0..3, q = 0, 1 in one
+    // half of the wave and 2, 3 in the other)
+    __device__ STG_AI static int mn_swz(int k)
+    {
+        return CPR == 16 ? (k & 3) | (((k >> 3) & 1) << 2) : ((k >> 1) & 1) | (((k >> 3) & 1) << 1);
+    }
+
+    const uint8_t *base; // first element of the tile (and of the group's K range)
+    int64_t ld;          // bytes between rows (K-contiguous) or K rows
+    int64_t k_bytes;     // K-contiguous: bytes of K; MN-major: K rows
+    int64_t span;        // K-contiguous: rows that exist; MN-major: bytes of a K row that exist
+    const uint8_t *sc;   // GL_Q8: scales of the first K row, at the tile's first column's block
+    int64_t ld_sc;
+    int voff[2][LD];     // [half][copy]: byte offset of this lane in the tile
+    int soff8[2][LD];    // GL_Q8: offset of its scale
+    int kc;              // K-contiguous: byte in the K tile of this lane's chunk
+    int rd[FR > 2 ? FR : 2]; // read offsets (K-contiguous: one per K step; else per fragment)
+    uint32_t code[2][LD][2], sbyte[2][LD]; // GL_Q8: in flight, by half
+
+    // wave_u: the wave's number; part: its place along this operand
+    __device__ STG_AI void init(int lane, int wave_u, int part)
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < LD; ++j) {
+                if constexpr (KC) {
+                    const int i = j * 64 + wave_u * 8 + (lane >> 3);
+                    const int row = (i / PIECE) * 2 * PIECE + h * PIECE + i % PIECE;
+                    kc = ((lane & 7) ^ ((lane >> 3) & 7)) * 16;
+                    voff[h][j] = row * (int)ld + kc;
+                } else {
+                    const int c = (j * 8 + wave_u) * 64 + lane; // chunk of the region
+                    const int k = c / CPR;
+                    const int i = ((c % CPR) ^ (mn_swz(k) << 1)) * 8; // region column
+                    const int col = (i / PIECE) * 2 * PIECE + h * PIECE + i % PIECE;
+                    if constexpr (LAYOUT == GL_Q8) {
+                        voff[h][j] = k * (int)ld + col;
+                        soff8[h][j] = k * (int)ld_sc + col / 32;
+                    } else {
+                        voff[h][j] = k * (int)ld + col * 2;
+                    }
+                }
+            }
+        const int l16 = lane & 15, q = lane >> 4;
+        if constexpr (KC) {
+            const int row = part * PIECE + l16;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                rd[s] = row * 128 + (((4 * s + q) ^ (row & 7)) << 4);
+        } else {
+            const int k = 8 * q + (l16 >> 2), f = mn_swz(k);
+#pragma unroll
+            for (int r = 0; r < FR; ++r)
+                rd[r] = k * PITCH + (((part * FR + r) ^ f) << 5) + (l16 & 3) * 8;
+        }
+    }
+
+    // Copy half h of K tile kt into `region` (LDS).
+    __device__ STG_AI void copy(uint8_t *region, auto half, int kt, int wave_u)
+    {
+        constexpr int h = decltype(half)::value;
+        if constexpr (KC) {
+            const __amdgpu_buffer_rsrc_t r = tile_rsrc(base, (span - 1) * ld + k_bytes);
+            // chunks past K read zeros: an offset outside every resource
+            const bool in = kt * 128 + kc < k_bytes;
+#pragma unroll
+            for (int j = 0; j < LD; ++j)
+                dma16(r, region + (j * 8 + wave_u) * 1024, in ? voff[h][j] : (int)0x80000000,
+                      kt * 128);
+        } else {
+            // the tile's K rows start the resource, so that every offset fits
+            // 32 bits and K rows past the end lie outside it
+            const int64_t left = k_bytes - (int64_t)kt * 64;
+            const __amdgpu_buffer_rsrc_t r =
+                epi_rsrc(base + (int64_t)kt * 64 * ld, left > 0 ? (left - 1) * ld + span : 0);
+            if constexpr (LAYOUT == GL_MN) {
+#pragma unroll
+                for (int j = 0; j < LD; ++j)
+                    dma16(r, region + (j * 8 + wave_u) * 1024, voff[h][j], 0);
+            } else {
+                const __amdgpu_buffer_rsrc_t rs = epi_rsrc(
+                    sc + (int64_t)kt * 64 * ld_sc, left > 0 ? (left - 1) * ld_sc + (span + 31) / 32 : 0);
+#pragma unroll
+                for (int j = 0; j < LD; ++j) {
+                    typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+                    const u2_t c = __builtin_bit_cast(
+                        u2_t, __builtin_amdgcn_raw_buffer_load_b64(r, voff[h][j], 0, 0));
+                    code[h][j][0] = c.x;
+                    code[h][j][1] = c.y;
+                    sbyte[h][j] = __builtin_amdgcn_raw_buffer_load_b8(rs, soff8[h][j], 0, 0);
+                }
+            }
+        }
+    }
+
+    // GL_Q8: half h's codes in registers, as 16-bit values into `region`.
+    __device__ STG_AI void store(uint8_t *region, auto half, int lane, int wave_u)
+    {
+        constexpr int h = decltype(half)::value;
+#pragma unroll
+        for (int j = 0; j < LD; ++j) {
+            const float s = e8m0(sbyte[h][j]);
+            u4_t v;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                typedef float f2_t __attribute__((ext_vector_type(2)));
+                const f2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[h][j][w], false);
+                const f2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[h][j][w], true);
+                const float x[4] = {lo.x * s, lo.y * s, hi.x * s, hi.y * s};
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const float p = clamp16<BF>(x[e]), q = clamp16<BF>(x[e + 1]);
+                    v[2 * w + e / 2] =
+                        BF ? f32_to_bf16_bits(p) | ((uint32_t)f32_to_bf16_bits(q) << 16)
+                           : f32_to_f16_bits(p) | ((uint32_t)f32_to_f16_bits(q) << 16);
+                }
+            }
+            *(u4_t *)(region + (j * 8 + wave_u) * 1024 + lane * 16) = v;
+        }
+    }
+
+    // Fragment r, K step s of this wave from `region`.
+    __device__ STG_AI u4_t read(const uint8_t *region, int r, int s) const
+    {
+        if constexpr (KC) {
+            return *(const u4_t *)(region + rd[s] + r * 16 * 128);
+        } else {
+            u4_t v;
+            lds_read_tr<2>(region + rd[r] + (32 * s) * PITCH, (uint32_t *)&v);
+            lds_read_tr<2>(region + rd[r] + (32 * s + 4) * PITCH, (uint32_t *)&v + 2);
+            return v;
+        }
+    }
+};
+
+template <class OP, bool W, int ALAY, int BLAY, int BM, int BN>
+__global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_grouped_tiled(GroupedArgs a,
+                                                                                    int tiles_m,
+                                                                                    int tiles_n)
+{
+    constexpr bool BF = std::is_same<OP, Op16BF16>::value;
+    constexpr int RA = BM / 2, RB = BN / 2;   // rows (columns) of a region
+    constexpr int WM = BM / 2, WN = BN / 4;   // a wave's block
+    constexpr int FA = WM / 32, FB = WN / 32; // fragments of one of its halves
+    typedef Operand<ALAY, RA, WM / 2, BF> OpA;
+    typedef Operand<BLAY, RB, WN / 2, BF> OpB;
+    // one LDS object per region and buffer: the compiler then knows that a
+    // copy in flight and a read of another region do not meet
+    __shared__ __attribute__((aligned(1024))) uint8_t a00[RA * 128], a10[RA * 128], a01[RA * 128],
+        a11[RA * 128], b00[RB * 128], b10[RB * 128], b01[RB * 128], b11[RB * 128];
+    auto reg_a = [&](auto half, auto buf) STG_AI -> uint8_t * {
+        if constexpr (decltype(buf)::value == 0)
+            return decltype(half)::value == 0 ? a00 : a10;
+        else
+            return decltype(half)::value == 0 ? a01 : a11;
+    };
+    auto reg_b = [&](auto half, auto buf) STG_AI -> uint8_t * {
+        if constexpr (decltype(buf)::value == 0)
+            return decltype(half)::value == 0 ? b00 : b10;
+        else
+            return decltype(half)::value == 0 ? b01 : b11;
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    GroupRows t;
+    int tm, tn;
+    int64_t M, K;
+    if constexpr (W) {
+        const int tile = xcd_tile(blockIdx.x, a.groups * tiles_m * tiles_n);
+        if (tile < 0)
+            return;
+        t.g = tile / (tiles_m * tiles_n);
+        tile_of(tile - t.g * tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        int b, e;
+        group_bounds(a, t.g, b, e);
+        t.r0 = __builtin_amdgcn_readfirstlane(b);
+        t.r1 = __builtin_amdgcn_readfirstlane(e);
+        M = a.K;
+        K = t.r1 - t.r0;
+    } else {
+        const int total = count_tiles<BM>(a, lane);
+        const int tile = xcd_tile(blockIdx.x, total * tiles_n);
+        if (tile < 0)
+            return;
+        tile_of(tile, total, tiles_n, tm, tn);
+        if (!find_tile<BM>(a, __builtin_amdgcn_readfirstlane(tm), lane, t))
+            return;
+        tm = t.tm;
+        M = t.r1 - t.r0;
+        K = a.K;
+    }
+    const int64_t m_blk = wave_uniform((int64_t)tm * BM), n_blk = wave_uniform((int64_t)tn * BN);
+    const int wm = wave >> 2, wn = wave & 3;
+
+    OpA A;
+    OpB B;
+    A.ld = a.lda * 2;
+    if constexpr (ALAY == GL_K) {
+        A.base = (const uint8_t *)a.A + (t.r0 + m_blk) * A.ld;
+        A.k_bytes = K * 2;
+        A.span = M - m_blk;
+    } else {
+        A.base = (const uint8_t *)a.A + t.r0 * A.ld + m_blk * 2;
+        A.k_bytes = K;
+        A.span = (M - m_blk) * 2;
+    }
+    constexpr int BE = BLAY == GL_Q8 ? 1 : 2;
+    B.ld = a.ldb * BE;
+    if constexpr (BLAY == GL_K) {
+        B.base = (const uint8_t *)a.B + ((int64_t)t.g * a.N + n_blk) * B.ld;
+        B.k_bytes = K * 2;
+        B.span = a.N - n_blk;
+    } else {
+        B.base = (const uint8_t *)a.B + (W ? t.r0 : (int64_t)t.g * a.K) * B.ld + n_blk * BE;
+        B.k_bytes = K;
+        B.span = (a.N - n_blk) * BE;
+    }
+    if constexpr (BLAY == GL_Q8) {
+        B.ld_sc = (a.N + 31) / 32;
+        B.sc = a.bs + t.r0 * B.ld_sc + n_blk / 32;
+    }
+    A.init(lane, wave, wm);
+    B.init(lane, wave, wn);
+
+    typename OP::acc_t acc[2 * FA][2 * FB];
+#pragma unroll
+    for (int i = 0; i < 2 * FA; ++i)
+#pragma unroll
+        for (int j = 0; j < 2 * FB; ++j)
+            acc[i][j] = typename OP::acc_t{};
+
+    const int KT = (int)((K + 63) / 64);
+    if (KT > 0) {
+        u4_t fa[FA][2], fb[2][FB][2];
+        auto read_a = [&](auto half, auto buf) STG_AI {
+#pragma unroll
+            for (int r = 0; r < FA; ++r)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    fa[r][s] = A.read(reg_a(half, buf), r, s);
+        };
+        auto read_b = [&](auto half, auto buf) STG_AI {
+#pragma unroll
+            for (int r = 0; r < FB; ++r)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    fb[decltype(half)::value][r][s] = B.read(reg_b(half, buf), r, s);
+        };
+        // keeps a memory phase's steps in their order
+        auto step = [&]() STG_AI {
+            STG_COMPILER_FENCE();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto barrier = [&]() STG_AI {
+            STG_COMPILER_FENCE();
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            STG_COMPILER_FENCE();
+        };
+        auto mfma = [&](auto ha, auto hb) STG_AI {
+            constexpr int P = decltype(ha)::value, Q = decltype(hb)::value;
+            barrier();
+            __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0)
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < FA; ++i)
+#pragma unroll
+                    for (int j = 0; j < FB; ++j)
+                        acc[P * FA + i][Q * FB + j] =
+                            OP::mma((const uint32_t *)&fa[i][s], (const uint32_t *)&fb[Q][j][s],
+                                    acc[P * FA + i][Q * FB + j]);
+            __builtin_amdgcn_s_setprio(0);
+            barrier();
+        };
+        // vector-memory instructions of the five clusters up to and with one
+        // that copies A (B): what may be in flight when the copies of the
+        // cluster before them have to be complete
+        constexpr int VA = OpA::VM, VB = OpB::VM;
+        constexpr int AFTER_B = 3 * VA + 2 * VB, AFTER_A = 2 * VA + 3 * VB;
+        constexpr bool Q8 = BLAY == GL_Q8;
+        // copies of B: tile t's half h; 8-bit: the registers loaded four
+        // clusters before go to LDS first (tile ts, buffer of that tile)
+        auto put_b = [&](auto half, auto buf) STG_AI {
+            if constexpr (Q8)
+                B.store(reg_b(half, buf), half, lane, wave);
+        };
+
+        // One K tile t in buffer P.  Cluster c copies, into the place that
+        // was read two clusters before: c = 0 A1 of t + 1 (buffer 1 - P), 1
+        // B0, 2 A0, 3 B1 of t + 2 (buffer P).  8-bit: cluster 1 first stores
+        // B0 of t + 1, loaded in cluster 1 of t - 1, cluster 3 B1 of t + 1.
+        auto tile = [&](auto pc, int kt) STG_AI {
+            using P = decltype(pc);
+            using N = std::integral_constant<int, 1 - P::value>;
+            read_a(I0{}, P{});
+            step();
+            A.copy(reg_a(I1{}, N{}), I1{}, kt + 1, wave);
+            step();
+            STG_WAIT_VMCNT(AFTER_B);
+            mfma(I0{}, I0{});
+            read_b(I1{}, P{});
+            put_b(I0{}, N{});
+            step();
+            B.copy(reg_b(I0{}, P{}), I0{}, kt + 2, wave);
+            step();
+            STG_WAIT_VMCNT(AFTER_A);
+            mfma(I0{}, I1{});
+            read_a(I1{}, P{});
+            step();
+            A.copy(reg_a(I0{}, P{}), I0{}, kt + 2, wave);
+            step();
+            STG_WAIT_VMCNT(AFTER_B);
+            mfma(I1{}, I0{});
+            read_b(I0{}, N{});
+            put_b(I1{}, N{});
+            step();
+            B.copy(reg_b(I1{}, P{}), I1{}, kt + 2, wave);
+            step();
+            STG_WAIT_VMCNT(AFTER_A);
+            mfma(I1{}, I1{});
+        };
+
+        // the copies of the clusters before cluster 0, in their order
+        B.copy(reg_b(I0{}, I0{}), I0{}, 0, wave);
+        A.copy(reg_a(I0{}, I0{}), I0{}, 0, wave);
+        B.copy(reg_b(I1{}, I0{}), I1{}, 0, wave);
+        A.copy(reg_a(I1{}, I0{}), I1{}, 0, wave);
+        put_b(I0{}, I0{});
+        B.copy(reg_b(I0{}, I1{}), I0{}, 1, wave);
+        A.copy(reg_a(I0{}, I1{}), I0{}, 1, wave);
+        put_b(I1{}, I0{});
+        B.copy(reg_b(I1{}, I1{}), I1{}, 1, wave);
+        STG_WAIT_VMCNT(3 * VB + 2 * VA);
+        __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0): 8-bit B's stores
+        barrier();
+        read_b(I0{}, I0{});
+        __builtin_amdgcn_s_waitcnt(0xC07F); // (read before anyone copies over it)
+        if (wave >= 4)
+            barrier(); // the trailing half starts one phase later
+        int kt = 0;
+        for (; kt + 1 < KT; kt += 2) {
+            tile(I0{}, kt);
+            tile(I1{}, kt + 1);
+        }
+        if (kt < KT)
+            tile(I0{}, kt);
+        if (wave < 4)
+            barrier();
+        STG_WAIT_VMCNT(0); // copies past the last tile, before LDS is reused
+        barrier();
+    }
+
+    // a wave's slab of 32 rows fits into the region of its number
+    static_assert(32 * (WN + 4) * 4 <= (RA < RB ? RA : RB) * 128, "epilogue slab");
+    uint8_t *slab = wave == 0   ? a00
+                    : wave == 1 ? a10
+                    : wave == 2 ? a01
+                    : wave == 3 ? a11
+                    : wave == 4 ? b00
+                    : wave == 5 ? b10
+                    : wave == 6 ? b01
+                                : b11;
+    EpiArgs e = group_epilogue(a, t.g, t.r0, M);
+    e.vec = a.vec;
+    const int64_t m0 = m_blk + wm * WM, n0 = n_blk + wn * WN;
+    uint32_t *const lds = (uint32_t *)slab;
+    if (a.d_kind == OUT_F32)
+        epilogue_slabs<OP, 2 * FA, 2 * FB, OUT_F32>(e, acc, m0, n0, lane, lds);
+    else if (a.d_kind == OUT_F16)
+        epilogue_slabs<OP, 2 * FA, 2 * FB, OUT_F16>(e, acc, m0, n0, lane, lds);
+    else
+        epilogue_slabs<OP, 2 * FA, 2 * FB, OUT_BF16>(e, acc, m0, n0, lane, lds);
+}
+
+} // namespace stg

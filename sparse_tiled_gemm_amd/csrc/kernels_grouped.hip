@@ -93,7 +93,9 @@ static hipError_t launch_generic(const GroupedArgs &a, hipStream_t s)
 
 hipError_t launch_grouped(int family, const GroupedArgs &a, hipStream_t s)
 {
-    (void)family;
+    if (family == GF_TILED_128 || family == GF_TILED_256)
+        return a.weights_mode ? launch_grouped_weights(family, a, s)
+                              : launch_grouped_rows(family, a, s);
     return a.bf16 ? launch_generic<OpBF16>(a, s) : launch_generic<OpF16>(a, s);
 }
 

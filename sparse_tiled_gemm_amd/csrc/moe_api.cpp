@@ -296,7 +296,8 @@ static bool normalise(gemm_grouped_desc_t &d)
             ld = mn > 0 ? mn : 1;
         return ld >= mn && ld > 0;
     };
-    return fix(d.lda, d.K) & fix(d.ldb, b_min) & fix(d.ldd, d.N);
+    const bool oka = fix(d.lda, d.K), okb = fix(d.ldb, b_min), okd = fix(d.ldd, d.N);
+    return oka && okb && okd;
 }
 
 gemm_status_t gemm_grouped_validate_desc(const gemm_grouped_desc_t *desc)
@@ -356,6 +357,19 @@ gemm_status_t gemm_grouped_validate_desc(const gemm_grouped_desc_t *desc)
     return ok();
 }
 
+// Can the LDS-tiled kernels serve this descriptor (ignoring pointer
+// alignment)?  They move 16-byte chunks: along K of a K-contiguous operand,
+// along N (K for A) of an MN-major one; offsets inside a tile's rows take
+// 32 bits.
+static bool grouped_tiled_ok(const gemm_grouped_desc_t &d)
+{
+    const bool w = d.mode == GEMM_GROUPED_WEIGHTS;
+    const bool b_mn = w || d.b_layout == GEMM_ROW_MAJOR;
+    const int64_t lim = (int64_t)1 << 21; // 256 rows of 2-byte elements below 2^30
+    return d.K % 8 == 0 && d.lda % 8 == 0 && d.ldb % 8 == 0 && (!b_mn || d.N % 8 == 0) &&
+           d.lda < lim && d.ldb < lim;
+}
+
 static const char *grouped_family_name(int f)
 {
     static const char *const n[GF_COUNT] = {"generic", "skinny", "tiled128", "tiled256"};
@@ -372,8 +386,18 @@ gemm_status_t gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_pl
     normalise(d);
     int dev = 0;
     CHECK(check_device(&dev, nullptr));
-    const int fam = GF_GENERIC;
-    if (d.algo != GEMM_ALGO_AUTO && d.algo != GEMM_ALGO_GENERIC)
+    const bool tiled = grouped_tiled_ok(d);
+    const int auto_tiled = d.rows >= 192 * (int64_t)d.groups ? GF_TILED_256 : GF_TILED_128;
+    int fam = -1;
+    switch (d.algo) {
+    case GEMM_ALGO_AUTO: fam = tiled ? auto_tiled : GF_GENERIC; break;
+    case GEMM_ALGO_GENERIC: fam = GF_GENERIC; break;
+    case GEMM_ALGO_TILED: fam = tiled ? auto_tiled : -1; break;
+    case GEMM_ALGO_TILED_128: fam = tiled ? GF_TILED_128 : -1; break;
+    case GEMM_ALGO_TILED_256: fam = tiled ? GF_TILED_256 : -1; break;
+    default: fam = -1;
+    }
+    if (fam < 0)
         return fail(GEMM_ERR_UNSUPPORTED, "requested algorithm cannot serve this problem");
     gemm_grouped_plan_t *p = new (std::nothrow) gemm_grouped_plan_t();
     if (!p)
@@ -451,7 +475,13 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_plan_t *plan, const void *A, c
     a.b_row = d.b_layout == GEMM_ROW_MAJOR;
     a.bf16 = d.a_type == GEMM_BF16;
     a.d_kind = d.d_type == GEMM_F32 ? OUT_F32 : d.d_type == GEMM_F16 ? OUT_F16 : OUT_BF16;
-    return launched(launch_grouped(plan->family, a, (hipStream_t)stream));
+    // the vector epilogue addresses 257 rows of C and D with 32-bit offsets
+    a.vec = (!d.has_c || aligned(C, 4 * (size_t)db)) && aligned(D, 4 * (size_t)db) &&
+            d.ldd % 4 == 0 && d.ldd * db < 0x7fffffff / 257;
+    int fam = plan->family;
+    if (fam != GF_GENERIC && (!aligned(A, 16) || !aligned(B, 16)))
+        fam = GF_GENERIC;
+    return launched(launch_grouped(fam, a, (hipStream_t)stream));
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoints

@@ -83,7 +83,11 @@ struct GroupedArgs {
     int b_row; // ROWS: B_g is K x N (row-major)
     int bf16;  // A's type
     int d_kind; // OutKind
+    int vec;    // rows of C and D allow the vector epilogue (EpiArgs::vec)
 };
+// one-launch grid limits and operand requirements are checked by the plan
+hipError_t launch_grouped_rows(int family, const GroupedArgs &a, hipStream_t s);    // tiled
+hipError_t launch_grouped_weights(int family, const GroupedArgs &a, hipStream_t s); // tiled
 hipError_t launch_grouped(int family, const GroupedArgs &a, hipStream_t s);
 
 } // namespace stg
