@@ -81,8 +81,11 @@ __device__ STG_AI inline int count_tiles(const GroupedArgs &a, int lane)
 }
 
 // One operand of the tile: where its rows (columns) lie and how it moves.
-// LAYOUT: GL_*; R: rows (columns) of a region; PIECE: rows of one wave in it
-// (region row i is tile row (i / PIECE) * 2 PIECE + half * PIECE + i % PIECE).
+// LAYOUT: GL_*; R: rows (columns) of a region; PIECE: rows of one wave in it.
+// Region row i of half h is tile row at(h, i): K-contiguous operands give each
+// wave neighbouring halves, so that its block of the output is one piece; an
+// MN-major region is a contiguous run, whose K rows are then fetched in 2 R
+// bytes at a time.
 template <int LAYOUT, int R, int PIECE, bool BF>
 struct Operand {
     static constexpr bool KC = LAYOUT == GL_K;
@@ -92,6 +95,11 @@ struct Operand {
     static constexpr int CPR = PITCH / 16;          // its 16-byte chunks
     static constexpr int FR = PIECE / 16;           // fragments of a wave
     static_assert(LD >= 1, "a region is at least one copy per wave");
+
+    __device__ STG_AI static int at(int h, int i)
+    {
+        return KC ? (i / PIECE) * 2 * PIECE + h * PIECE + i % PIECE : h * R + i;
+    }
 
     // (a transposing read touches K rows 8 q + 4 t + 0..3, q = 0, 1 in one
     // half of the wave and 2, 3 in the other)
@@ -121,14 +129,14 @@ struct Operand {
             for (int j = 0; j < LD; ++j) {
                 if constexpr (KC) {
                     const int i = j * 64 + wave_u * 8 + (lane >> 3);
-                    const int row = (i / PIECE) * 2 * PIECE + h * PIECE + i % PIECE;
+                    const int row = at(h, i);
                     kc = ((lane & 7) ^ ((lane >> 3) & 7)) * 16;
                     voff[h][j] = row * (int)ld + kc;
                 } else {
                     const int c = (j * 8 + wave_u) * 64 + lane; // chunk of the region
                     const int k = c / CPR;
                     const int i = ((c % CPR) ^ (mn_swz(k) << 1)) * 8; // region column
-                    const int col = (i / PIECE) * 2 * PIECE + h * PIECE + i % PIECE;
+                    const int col = at(h, i);
                     if constexpr (LAYOUT == GL_Q8) {
                         voff[h][j] = k * (int)ld + col;
                         soff8[h][j] = k * (int)ld_sc + col / 32;
@@ -195,20 +203,35 @@ struct Operand {
         constexpr int h = decltype(half)::value;
 #pragma unroll
         for (int j = 0; j < LD; ++j) {
-            const float s = e8m0(sbyte[h][j]);
+            const uint32_t sb = sbyte[h][j];
             u4_t v;
+            // scales that cannot take a code past the type's range (448 *
+            // 2^(sb - 127)), nor are NaN or subnormal: two values at a time
+            if (sb - 1u < (BF ? 246u : 134u)) {
+                const float s = __builtin_bit_cast(float, sb << 23);
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                typedef float f2_t __attribute__((ext_vector_type(2)));
-                const f2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[h][j][w], false);
-                const f2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[h][j][w], true);
-                const float x[4] = {lo.x * s, lo.y * s, hi.x * s, hi.y * s};
+                for (int w = 0; w < 4; ++w) {
+                    const int c = (int)code[h][j][w >> 1];
+                    if constexpr (BF)
+                        v[w] = __builtin_bit_cast(
+                            uint32_t, w & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, true)
+                                            : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, false));
+                    else
+                        v[w] = __builtin_bit_cast(
+                            uint32_t, w & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, s, true)
+                                            : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, s, false));
+                }
+            } else {
+                const float s = e8m0(sb);
 #pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const float p = clamp16<BF>(x[e]), q = clamp16<BF>(x[e + 1]);
-                    v[2 * w + e / 2] =
-                        BF ? f32_to_bf16_bits(p) | ((uint32_t)f32_to_bf16_bits(q) << 16)
-                           : f32_to_f16_bits(p) | ((uint32_t)f32_to_f16_bits(q) << 16);
+                for (int w = 0; w < 4; ++w) {
+                    typedef float f2_t __attribute__((ext_vector_type(2)));
+                    const int c = (int)code[h][j][w >> 1];
+                    const f2_t x = w & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(c, true)
+                                         : __builtin_amdgcn_cvt_pk_f32_fp8(c, false);
+                    const float p = clamp16<BF>(x.x * s), q = clamp16<BF>(x.y * s);
+                    v[w] = BF ? f32_to_bf16_bits(p) | ((uint32_t)f32_to_bf16_bits(q) << 16)
+                              : f32_to_f16_bits(p) | ((uint32_t)f32_to_f16_bits(q) << 16);
                 }
             }
             *(u4_t *)(region + (j * 8 + wave_u) * 1024 + lane * 16) = v;
@@ -265,11 +288,14 @@ __global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_grouped_t
     int tm, tn;
     int64_t M, K;
     if constexpr (W) {
-        const int tile = xcd_tile(blockIdx.x, a.groups * tiles_m * tiles_n);
-        if (tile < 0)
+        // every XCD takes an eighth of each group's tiles: groups differ in
+        // length, and whole groups would leave some XCDs idle at the end
+        const int per = (tiles_m * tiles_n + 7) >> 3, slot = blockIdx.x >> 3;
+        const int tile = (blockIdx.x & 7) * per + slot % per;
+        if (tile >= tiles_m * tiles_n)
             return;
-        t.g = tile / (tiles_m * tiles_n);
-        tile_of(tile - t.g * tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        t.g = slot / per;
+        tile_of(tile, tiles_m, tiles_n, tm, tn);
         int b, e;
         group_bounds(a, t.g, b, e);
         t.r0 = __builtin_amdgcn_readfirstlane(b);
@@ -465,14 +491,34 @@ __global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_grouped_t
                                 : b11;
     EpiArgs e = group_epilogue(a, t.g, t.r0, M);
     e.vec = a.vec;
-    const int64_t m0 = m_blk + wm * WM, n0 = n_blk + wn * WN;
     uint32_t *const lds = (uint32_t *)slab;
-    if (a.d_kind == OUT_F32)
-        epilogue_slabs<OP, 2 * FA, 2 * FB, OUT_F32>(e, acc, m0, n0, lane, lds);
-    else if (a.d_kind == OUT_F16)
-        epilogue_slabs<OP, 2 * FA, 2 * FB, OUT_F16>(e, acc, m0, n0, lane, lds);
-    else
-        epilogue_slabs<OP, 2 * FA, 2 * FB, OUT_BF16>(e, acc, m0, n0, lane, lds);
+    // the wave's block, in as many pieces as its rows and columns lie in
+    constexpr int PA = OpA::KC ? 1 : 2, PB = OpB::KC ? 1 : 2;
+    auto store = [&](auto p, auto q) STG_AI {
+        constexpr int FM = 2 * FA / PA, FN = 2 * FB / PB;
+        constexpr int I = decltype(p)::value * FM, J = decltype(q)::value * FN;
+        const int64_t m0 = m_blk + OpA::at(decltype(p)::value, wm * (WM / 2));
+        const int64_t n0 = n_blk + OpB::at(decltype(q)::value, wn * (WN / 2));
+        typename OP::acc_t part[FM][FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                part[i][j] = acc[I + i][J + j];
+        if (a.d_kind == OUT_F32)
+            epilogue_slabs<OP, FM, FN, OUT_F32>(e, part, m0, n0, lane, lds);
+        else if (a.d_kind == OUT_F16)
+            epilogue_slabs<OP, FM, FN, OUT_F16>(e, part, m0, n0, lane, lds);
+        else
+            epilogue_slabs<OP, FM, FN, OUT_BF16>(e, part, m0, n0, lane, lds);
+    };
+    store(I0{}, I0{});
+    if constexpr (PB == 2)
+        store(I0{}, I1{});
+    if constexpr (PA == 2)
+        store(I1{}, I0{});
+    if constexpr (PA == 2 && PB == 2)
+        store(I1{}, I1{});
 }
 
 } // namespace stg

@@ -9,8 +9,8 @@ template <class OP, int BLAY, int BM, int BN>
 static hipError_t launch_t(const GroupedArgs &a, hipStream_t s)
 {
     const int tiles_m = (int)((a.K + BM - 1) / BM), tiles_n = (int)((a.N + BN - 1) / BN);
-    const int64_t tiles = (int64_t)a.groups * tiles_m * tiles_n;
-    const dim3 grid((unsigned)((tiles + 7) / 8 * 8));
+    const int64_t per_xcd = ((int64_t)tiles_m * tiles_n + 7) / 8;
+    const dim3 grid((unsigned)(per_xcd * 8 * a.groups));
     hipLaunchKernelGGL((k_grouped_tiled<OP, true, GL_MN, BLAY, BM, BN>), grid, dim3(512), 0, s, a,
                        tiles_m, tiles_n);
     return hipGetLastError();
