@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libstgemm.so")
 SOURCES = ["gemm_api.cpp", "kernels_dense.hip", "kernels_sparse.hip", "kernels_mx.hip",
            "kernels_w4.hip", "kernels_mn.hip", "kernels_diag.hip", "kernels_k16.hip",
            "moe_api.cpp", "kernels_route.hip", "kernels_q8.hip", "kernels_grouped.hip",
-           "kernels_grouped_rows.hip", "kernels_grouped_weights.hip"]
+           "kernels_grouped_rows.hip", "kernels_grouped_weights.hip",
+           "kernels_grouped_skinny.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -21,18 +21,58 @@ __device__ STG_AI inline void group_bounds(const GroupedArgs &a, int g, int &b, 
     e = max(min(max(a.offsets[g + 1], 0), rows), b);
 }
 
-// Tile `tile` of the groups' BM-row tiles counted one group after the other;
-// false past the last one.  The groups are scanned 64 at a time, one per
-// lane; every lane of the wave gets the (uniform) answer.
-template <int BM>
-__device__ STG_AI inline bool find_tile(const GroupedArgs &a, int tile, int lane, GroupRows &out)
+// BM-row tiles of a group of n rows.  SHORT: only those with more than BM/2
+// rows (long); a remainder of at most BM/2 is a short tile.
+template <int BM, bool SHORT>
+__device__ STG_AI inline int long_tiles(int n)
 {
+    return SHORT ? (n + BM / 2 - 1) / BM : (n + BM - 1) / BM;
+}
+template <int BM>
+__device__ STG_AI inline int short_tiles(int n)
+{
+    return (n + BM - 1) / BM - (n + BM / 2 - 1) / BM;
+}
+
+// Long and short tiles of all groups.
+template <int BM, bool SHORT>
+__device__ STG_AI inline void count_tiles(const GroupedArgs &a, int lane, int &n_long, int &n_short)
+{
+    int l = 0, s = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += 64)
+        if (g0 + lane < a.groups) {
+            int b, e;
+            group_bounds(a, g0 + lane, b, e);
+            l += long_tiles<BM, SHORT>(e - b);
+            s += SHORT ? short_tiles<BM>(e - b) : 0;
+        }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        l += __shfl_xor(l, d);
+        if (SHORT)
+            s += __shfl_xor(s, d);
+    }
+    n_long = __builtin_amdgcn_readfirstlane(l);
+    n_short = __builtin_amdgcn_readfirstlane(s);
+}
+
+// Tile `tile` of the groups' long tiles counted one group after the other,
+// then (SHORT, from n_long on) of their short ones; false past the last.  The
+// groups are scanned 64 at a time, one per lane; every lane of the wave gets
+// the (uniform) answer.
+template <int BM, bool SHORT = false>
+__device__ STG_AI inline bool find_tile(const GroupedArgs &a, int tile, int n_long, int lane,
+                                        GroupRows &out)
+{
+    const bool second = SHORT && tile >= n_long;
+    if (second)
+        tile -= n_long;
     int done = 0; // tiles of the groups before g0
     for (int g0 = 0; g0 < a.groups; g0 += 64) {
         int b = 0, e = 0;
         if (g0 + lane < a.groups)
             group_bounds(a, g0 + lane, b, e);
-        const int n = (e - b + BM - 1) / BM;
+        const int n = second ? short_tiles<BM>(e - b) : long_tiles<BM, SHORT>(e - b);
         int incl = n;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -45,7 +85,8 @@ __device__ STG_AI inline bool find_tile(const GroupedArgs &a, int tile, int lane
             out.g = g0 + l;
             out.r0 = __builtin_amdgcn_readlane(b, l);
             out.r1 = __builtin_amdgcn_readlane(e, l);
-            out.tm = tile - done - __builtin_amdgcn_readlane(incl - n, l);
+            out.tm = second ? (int)((out.r1 - out.r0) / BM)
+                            : tile - done - __builtin_amdgcn_readlane(incl - n, l);
             return true;
         }
         done += __builtin_amdgcn_readlane(incl, 63);

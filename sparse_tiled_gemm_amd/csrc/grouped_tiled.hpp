@@ -63,23 +63,6 @@ __device__ STG_AI inline void tile_of(int t, int tiles_m, int tiles_n, int &tm, 
     tn = in / rows;
 }
 
-// Row tiles of all groups.
-template <int BM>
-__device__ STG_AI inline int count_tiles(const GroupedArgs &a, int lane)
-{
-    int n = 0;
-    for (int g0 = 0; g0 < a.groups; g0 += 64)
-        if (g0 + lane < a.groups) {
-            int b, e;
-            group_bounds(a, g0 + lane, b, e);
-            n += (e - b + BM - 1) / BM;
-        }
-#pragma unroll
-    for (int d = 32; d; d >>= 1)
-        n += __shfl_xor(n, d);
-    return __builtin_amdgcn_readfirstlane(n);
-}
-
 // One operand of the tile: where its rows (columns) lie and how it moves.
 // LAYOUT: GL_*; R: rows (columns) of a region; PIECE: rows of one wave in it.
 // Region row i of half h is tile row at(h, i): K-contiguous operands give each
@@ -252,10 +235,26 @@ struct Operand {
     }
 };
 
+// The LDS regions of a tile, one object per region and buffer: the compiler
+// then knows that a copy in flight and a read of another region do not meet.
+// [half][buffer] of A, then of B.
+struct Regions {
+    uint8_t *a00, *a10, *a01, *a11, *b00, *b10, *b01, *b11;
+};
+// Bytes of a region of R rows (columns): a wave's epilogue slab fits too.
+template <int R, int WN>
+constexpr int region_bytes()
+{
+    constexpr int slab = 32 * (WN + 4) * 4;
+    return R * 128 > slab ? R * 128 : (slab + 1023) / 1024 * 1024;
+}
+
+// One BM x BN tile of group t at (m_blk, n_blk); M, K: its group's rows (of
+// the output) and sum.
 template <class OP, bool W, int ALAY, int BLAY, int BM, int BN>
-__global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_grouped_tiled(GroupedArgs a,
-                                                                                    int tiles_m,
-                                                                                    int tiles_n)
+__device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
+                                        int64_t n_blk, int64_t M, int64_t K, int lane, int wave,
+                                        const Regions &L)
 {
     constexpr bool BF = std::is_same<OP, Op16BF16>::value;
     constexpr int RA = BM / 2, RB = BN / 2;   // rows (columns) of a region
@@ -263,58 +262,20 @@ __global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_grouped_t
     constexpr int FA = WM / 32, FB = WN / 32; // fragments of one of its halves
     typedef Operand<ALAY, RA, WM / 2, BF> OpA;
     typedef Operand<BLAY, RB, WN / 2, BF> OpB;
-    // one LDS object per region and buffer: the compiler then knows that a
-    // copy in flight and a read of another region do not meet
-    __shared__ __attribute__((aligned(1024))) uint8_t a00[RA * 128], a10[RA * 128], a01[RA * 128],
-        a11[RA * 128], b00[RB * 128], b10[RB * 128], b01[RB * 128], b11[RB * 128];
     auto reg_a = [&](auto half, auto buf) STG_AI -> uint8_t * {
         if constexpr (decltype(buf)::value == 0)
-            return decltype(half)::value == 0 ? a00 : a10;
+            return decltype(half)::value == 0 ? L.a00 : L.a10;
         else
-            return decltype(half)::value == 0 ? a01 : a11;
+            return decltype(half)::value == 0 ? L.a01 : L.a11;
     };
     auto reg_b = [&](auto half, auto buf) STG_AI -> uint8_t * {
         if constexpr (decltype(buf)::value == 0)
-            return decltype(half)::value == 0 ? b00 : b10;
+            return decltype(half)::value == 0 ? L.b00 : L.b10;
         else
-            return decltype(half)::value == 0 ? b01 : b11;
+            return decltype(half)::value == 0 ? L.b01 : L.b11;
     };
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
-
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    GroupRows t;
-    int tm, tn;
-    int64_t M, K;
-    if constexpr (W) {
-        // every XCD takes an eighth of each group's tiles: groups differ in
-        // length, and whole groups would leave some XCDs idle at the end
-        const int per = (tiles_m * tiles_n + 7) >> 3, slot = blockIdx.x >> 3;
-        const int tile = (blockIdx.x & 7) * per + slot % per;
-        if (tile >= tiles_m * tiles_n)
-            return;
-        t.g = slot / per;
-        tile_of(tile, tiles_m, tiles_n, tm, tn);
-        int b, e;
-        group_bounds(a, t.g, b, e);
-        t.r0 = __builtin_amdgcn_readfirstlane(b);
-        t.r1 = __builtin_amdgcn_readfirstlane(e);
-        M = a.K;
-        K = t.r1 - t.r0;
-    } else {
-        const int total = count_tiles<BM>(a, lane);
-        const int tile = xcd_tile(blockIdx.x, total * tiles_n);
-        if (tile < 0)
-            return;
-        tile_of(tile, total, tiles_n, tm, tn);
-        if (!find_tile<BM>(a, __builtin_amdgcn_readfirstlane(tm), lane, t))
-            return;
-        tm = t.tm;
-        M = t.r1 - t.r0;
-        K = a.K;
-    }
-    const int64_t m_blk = wave_uniform((int64_t)tm * BM), n_blk = wave_uniform((int64_t)tn * BN);
     const int wm = wave >> 2, wn = wave & 3;
 
     OpA A;
@@ -359,16 +320,16 @@ __global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_grouped_t
         u4_t fa[FA][2], fb[2][FB][2];
         auto read_a = [&](auto half, auto buf) STG_AI {
 #pragma unroll
-            for (int r = 0; r < FA; ++r)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                for (int r = 0; r < FA; ++r)
                     fa[r][s] = A.read(reg_a(half, buf), r, s);
         };
         auto read_b = [&](auto half, auto buf) STG_AI {
 #pragma unroll
-            for (int r = 0; r < FB; ++r)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                for (int r = 0; r < FB; ++r)
                     fb[decltype(half)::value][r][s] = B.read(reg_b(half, buf), r, s);
         };
         // keeps a memory phase's steps in their order
@@ -479,16 +440,15 @@ __global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_grouped_t
         barrier();
     }
 
-    // a wave's slab of 32 rows fits into the region of its number
-    static_assert(32 * (WN + 4) * 4 <= (RA < RB ? RA : RB) * 128, "epilogue slab");
-    uint8_t *slab = wave == 0   ? a00
-                    : wave == 1 ? a10
-                    : wave == 2 ? a01
-                    : wave == 3 ? a11
-                    : wave == 4 ? b00
-                    : wave == 5 ? b10
-                    : wave == 6 ? b01
-                                : b11;
+    // a wave's slab of 32 rows lies in the region of its number
+    uint8_t *slab = wave == 0   ? L.a00
+                    : wave == 1 ? L.a10
+                    : wave == 2 ? L.a01
+                    : wave == 3 ? L.a11
+                    : wave == 4 ? L.b00
+                    : wave == 5 ? L.b10
+                    : wave == 6 ? L.b01
+                                : L.b11;
     EpiArgs e = group_epilogue(a, t.g, t.r0, M);
     e.vec = a.vec;
     uint32_t *const lds = (uint32_t *)slab;
@@ -519,6 +479,90 @@ __global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_grouped_t
         store(I1{}, I0{});
     if constexpr (PA == 2 && PB == 2)
         store(I1{}, I1{});
+}
+
+// The kernel.  The rows' product with 256-row tiles (SHORT) cuts a group's
+// last rows, if they are at most 128, as a 128 x 256 tile (0.69 of the time
+// of a 256 x 256 one), and lets these come last, so that the compute units
+// that finish their long tiles first take them.  If the long tiles past the
+// last full round of the compute units and the short ones then fit one round
+// as short tiles, these long ones are cut in two as well.
+template <class OP, bool W, int ALAY, int BLAY, int BM, int BN, bool SHORT>
+__global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_grouped_tiled(GroupedArgs a,
+                                                                                    int tiles_m,
+                                                                                    int tiles_n)
+{
+    constexpr int AB = region_bytes<BM / 2, BN / 4>(), BB = region_bytes<BN / 2, BN / 4>();
+    __shared__ __attribute__((aligned(1024))) uint8_t a00[AB], a10[AB], a01[AB], a11[AB], b00[BB],
+        b10[BB], b01[BB], b11[BB];
+    const Regions L = {a00, a10, a01, a11, b00, b10, b01, b11};
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    GroupRows t;
+    if constexpr (W) {
+        // every XCD takes an eighth of each group's tiles: groups differ in
+        // length, and whole groups would leave some XCDs idle at the end
+        const int per = (tiles_m * tiles_n + 7) >> 3, slot = blockIdx.x >> 3;
+        const int tile = (blockIdx.x & 7) * per + slot % per;
+        if (tile >= tiles_m * tiles_n)
+            return;
+        int tm, tn, b, e;
+        t.g = slot / per;
+        tile_of(tile, tiles_m, tiles_n, tm, tn);
+        group_bounds(a, t.g, b, e);
+        t.r0 = __builtin_amdgcn_readfirstlane(b);
+        t.r1 = __builtin_amdgcn_readfirstlane(e);
+        tile_body<OP, W, ALAY, BLAY, BM, BN>(a, t, wave_uniform((int64_t)tm * BM),
+                                             wave_uniform((int64_t)tn * BN), a.K, t.r1 - t.r0, lane,
+                                             wave, L);
+    } else {
+        int n_long, n_short;
+        count_tiles<BM, SHORT>(a, lane, n_long, n_short);
+        const int total = n_long * tiles_n, shorts = n_short * tiles_n;
+        int tm, tn, part = -1; // part: half of a long tile
+        if constexpr (SHORT) {
+            int id = blockIdx.x, whole = total;
+            const int rest = total % a.num_cu;
+            if (2 * rest + shorts <= a.num_cu && (total - rest) % 8 == 0)
+                whole -= rest;
+            if (id >= (whole + 7) / 8 * 8) {
+                id -= (whole + 7) / 8 * 8;
+                if (id < 2 * (total - whole)) {
+                    part = id & 1;
+                    tile_of(whole + (id >> 1), n_long, tiles_n, tm, tn);
+                } else {
+                    id -= 2 * (total - whole);
+                    if (id >= shorts)
+                        return;
+                    tm = n_long + id / tiles_n;
+                    tn = id % tiles_n;
+                }
+            } else {
+                id = xcd_tile(id, whole);
+                if (id < 0)
+                    return;
+                tile_of(id, n_long, tiles_n, tm, tn);
+            }
+        } else {
+            const int id = xcd_tile(blockIdx.x, total);
+            if (id < 0)
+                return;
+            tile_of(id, n_long, tiles_n, tm, tn);
+        }
+        if (!find_tile<BM, SHORT>(a, __builtin_amdgcn_readfirstlane(tm), n_long, lane, t))
+            return;
+        const int64_t m = wave_uniform((int64_t)t.tm * BM), n = wave_uniform((int64_t)tn * BN);
+        const int64_t M = t.r1 - t.r0;
+        if constexpr (SHORT) {
+            if (part >= 0 || M - m <= BM / 2) {
+                const int64_t mh = m + (part > 0 ? BM / 2 : 0);
+                if (mh < M)
+                    tile_body<OP, W, ALAY, BLAY, BM / 2, BN>(a, t, mh, n, M, a.K, lane, wave, L);
+                return;
+            }
+        }
+        tile_body<OP, W, ALAY, BLAY, BM, BN>(a, t, m, n, M, a.K, lane, wave, L);
+    }
 }
 
 } // namespace stg

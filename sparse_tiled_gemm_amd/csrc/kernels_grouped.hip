@@ -29,7 +29,7 @@ __global__ __launch_bounds__(256) void k_grouped_generic(GroupedArgs a, int tile
         M = a.K;
         K = t.r1 - t.r0;
     } else {
-        if (!find_tile<64>(a, rest, lane, t))
+        if (!find_tile<64>(a, rest, 0, lane, t))
             return;
         m0 = (int64_t)t.tm * 64;
         M = t.r1 - t.r0;
@@ -93,7 +93,9 @@ static hipError_t launch_generic(const GroupedArgs &a, hipStream_t s)
 
 hipError_t launch_grouped(int family, const GroupedArgs &a, hipStream_t s)
 {
-    if (family == GF_TILED_128 || family == GF_TILED_256)
+    if (family == GF_SKINNY)
+        return launch_grouped_skinny(a, s);
+    if (family != GF_GENERIC)
         return a.weights_mode ? launch_grouped_weights(family, a, s)
                               : launch_grouped_rows(family, a, s);
     return a.bf16 ? launch_generic<OpBF16>(a, s) : launch_generic<OpF16>(a, s);

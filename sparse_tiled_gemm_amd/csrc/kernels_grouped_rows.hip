@@ -9,9 +9,11 @@ static hipError_t launch_t(const GroupedArgs &a, hipStream_t s)
 {
     const int tiles_n = (int)((a.N + BN - 1) / BN);
     const int64_t tiles = max_row_tiles<BM>(a) * tiles_n;
-    const dim3 grid((unsigned)((tiles + 7) / 8 * 8));
-    hipLaunchKernelGGL((k_grouped_tiled<OP, false, GL_K, BLAY, BM, BN>), grid, dim3(512), 0, s, a, 0,
-                       tiles_n);
+    constexpr bool SHORT = BM == 256;
+    const int64_t extra = SHORT ? a.num_cu / 2 : 0; // second halves of the last long tiles
+    const dim3 grid((unsigned)((tiles + extra + 7) / 8 * 8 + 8));
+    hipLaunchKernelGGL((k_grouped_tiled<OP, false, GL_K, BLAY, BM, BN, SHORT>), grid, dim3(512), 0, s,
+                       a, 0, tiles_n);
     return hipGetLastError();
 }
 
@@ -20,6 +22,8 @@ static hipError_t launch_op(int family, const GroupedArgs &a, hipStream_t s)
 {
     if (family == GF_TILED_256)
         return a.b_row ? launch_t<OP, GL_MN, 256, 256>(a, s) : launch_t<OP, GL_K, 256, 256>(a, s);
+    if (family == GF_TILED_128X256)
+        return a.b_row ? launch_t<OP, GL_MN, 128, 256>(a, s) : launch_t<OP, GL_K, 128, 256>(a, s);
     return a.b_row ? launch_t<OP, GL_MN, 128, 128>(a, s) : launch_t<OP, GL_K, 128, 128>(a, s);
 }
 

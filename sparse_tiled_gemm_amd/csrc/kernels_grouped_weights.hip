@@ -11,7 +11,7 @@ static hipError_t launch_t(const GroupedArgs &a, hipStream_t s)
     const int tiles_m = (int)((a.K + BM - 1) / BM), tiles_n = (int)((a.N + BN - 1) / BN);
     const int64_t per_xcd = ((int64_t)tiles_m * tiles_n + 7) / 8;
     const dim3 grid((unsigned)(per_xcd * 8 * a.groups));
-    hipLaunchKernelGGL((k_grouped_tiled<OP, true, GL_MN, BLAY, BM, BN>), grid, dim3(512), 0, s, a,
+    hipLaunchKernelGGL((k_grouped_tiled<OP, true, GL_MN, BLAY, BM, BN, false>), grid, dim3(512), 0, s, a,
                        tiles_m, tiles_n);
     return hipGetLastError();
 }
@@ -21,6 +21,8 @@ static hipError_t launch_op(int family, const GroupedArgs &a, hipStream_t s)
 {
     if (family == GF_TILED_256)
         return a.bs ? launch_t<OP, GL_Q8, 256, 256>(a, s) : launch_t<OP, GL_MN, 256, 256>(a, s);
+    if (family == GF_TILED_128X256)
+        return a.bs ? launch_t<OP, GL_Q8, 128, 256>(a, s) : launch_t<OP, GL_MN, 128, 256>(a, s);
     return a.bs ? launch_t<OP, GL_Q8, 128, 128>(a, s) : launch_t<OP, GL_MN, 128, 128>(a, s);
 }
 

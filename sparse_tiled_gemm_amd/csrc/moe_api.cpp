@@ -18,7 +18,7 @@ using namespace stg;
 struct gemm_grouped_plan {
     gemm_grouped_desc_t d; // normalised: packed leading dimensions filled in
     int family;            // stg::GroupedFamily
-    int device;
+    int device, num_cu;
     char name[64];
 };
 
@@ -372,7 +372,8 @@ static bool grouped_tiled_ok(const gemm_grouped_desc_t &d)
 
 static const char *grouped_family_name(int f)
 {
-    static const char *const n[GF_COUNT] = {"generic", "skinny", "tiled128", "tiled256"};
+    static const char *const n[GF_COUNT] = {"generic", "skinny", "tiled128", "tiled128x256",
+                                             "tiled256"};
     return n[f];
 }
 
@@ -385,17 +386,37 @@ gemm_status_t gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_pl
     gemm_grouped_desc_t d = *desc;
     normalise(d);
     int dev = 0;
-    CHECK(check_device(&dev, nullptr));
+    DeviceInfo di;
+    CHECK(check_device(&dev, &di));
     const bool tiled = grouped_tiled_ok(d);
     const int auto_tiled = d.rows >= 192 * (int64_t)d.groups ? GF_TILED_256 : GF_TILED_128;
+    // Few rows per group: B's stream bounds the product (the plan cannot see
+    // the groups' bounds; every family serves groups of any length).  With B
+    // 32 x 4096 x 2048 the skinny kernel and the 128 x 128 tile took 109 and
+    // 123 us at 4 rows per group, 138 and 125 us at 16 (row-major B: 126 and
+    // 137 us at 16, 145 and 145 us at 32); where the 128-wide tiles leave
+    // compute units idle its split along K helps longer: 4 groups of 1024 x
+    // 2048, 8 and 20 us at 4 rows each, 10 and 20 at 16, 20 and 20 at 64.
+    const bool skinny = tiled && d.mode == GEMM_GROUPED_ROWS;
+    const int64_t wide = (ceil_div(d.rows, 128) + (d.groups < d.rows ? d.groups : d.rows)) *
+                         ceil_div(d.N, 128);
+    const int64_t few_rows = wide < di.num_cu ? 48 : d.b_layout == GEMM_ROW_MAJOR ? 24 : 10;
+    const bool few = d.rows <= few_rows * d.groups;
     int fam = -1;
     switch (d.algo) {
-    case GEMM_ALGO_AUTO: fam = tiled ? auto_tiled : GF_GENERIC; break;
+    case GEMM_ALGO_AUTO: fam = skinny && few ? GF_SKINNY : tiled ? auto_tiled : GF_GENERIC; break;
+    case GEMM_ALGO_SKINNY: fam = skinny ? GF_SKINNY : -1; break;
     case GEMM_ALGO_GENERIC: fam = GF_GENERIC; break;
     case GEMM_ALGO_TILED: fam = tiled ? auto_tiled : -1; break;
     case GEMM_ALGO_TILED_128: fam = tiled ? GF_TILED_128 : -1; break;
     case GEMM_ALGO_TILED_256: fam = tiled ? GF_TILED_256 : -1; break;
     default: fam = -1;
+    }
+    if (const char *force = getenv("STGEMM_FORCE_KERNEL")) { // tuning override
+        for (int f = GF_GENERIC; f < GF_COUNT; ++f)
+            if (strcmp(force, grouped_family_name(f)) == 0 &&
+                (f == GF_GENERIC || (f == GF_SKINNY ? skinny : tiled)))
+                fam = f;
     }
     if (fam < 0)
         return fail(GEMM_ERR_UNSUPPORTED, "requested algorithm cannot serve this problem");
@@ -404,6 +425,7 @@ gemm_status_t gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_pl
         return fail(GEMM_ERR_INVALID_VALUE, "out of host memory");
     p->d = d;
     p->device = dev;
+    p->num_cu = di.num_cu;
     p->family = fam;
     snprintf(p->name, sizeof p->name, "grouped_%s_%s_%s%s%s",
              d.mode == GEMM_GROUPED_WEIGHTS ? "weights" : "rows", grouped_family_name(fam),
@@ -476,6 +498,7 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_plan_t *plan, const void *A, c
     a.bf16 = d.a_type == GEMM_BF16;
     a.d_kind = d.d_type == GEMM_F32 ? OUT_F32 : d.d_type == GEMM_F16 ? OUT_F16 : OUT_BF16;
     // the vector epilogue addresses 257 rows of C and D with 32-bit offsets
+    a.num_cu = plan->num_cu;
     a.vec = (!d.has_c || aligned(C, 4 * (size_t)db)) && aligned(D, 4 * (size_t)db) &&
             d.ldd % 4 == 0 && d.ldd * db < 0x7fffffff / 257;
     int fam = plan->family;

@@ -68,7 +68,14 @@ hipError_t launch_swiglu_backward(const Q8Args &a, hipStream_t s);
 
 // ---------------------------------------------------------------- grouped products
 
-enum GroupedFamily { GF_GENERIC = 0, GF_SKINNY, GF_TILED_128, GF_TILED_256, GF_COUNT };
+enum GroupedFamily {
+    GF_GENERIC = 0,
+    GF_SKINNY,
+    GF_TILED_128,    // 128 x 128, two workgroups per compute unit
+    GF_TILED_128X256,
+    GF_TILED_256,
+    GF_COUNT
+};
 
 struct GroupedArgs {
     int weights_mode; // 0: ROWS, 1: WEIGHTS
@@ -83,10 +90,12 @@ struct GroupedArgs {
     int b_row; // ROWS: B_g is K x N (row-major)
     int bf16;  // A's type
     int d_kind; // OutKind
+    int num_cu; // compute units of the device
     int vec;    // rows of C and D allow the vector epilogue (EpiArgs::vec)
 };
 // one-launch grid limits and operand requirements are checked by the plan
 hipError_t launch_grouped_rows(int family, const GroupedArgs &a, hipStream_t s);    // tiled
+hipError_t launch_grouped_skinny(const GroupedArgs &a, hipStream_t s); // rows
 hipError_t launch_grouped_weights(int family, const GroupedArgs &a, hipStream_t s); // tiled
 hipError_t launch_grouped(int family, const GroupedArgs &a, hipStream_t s);
 

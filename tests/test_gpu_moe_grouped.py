@@ -1,5 +1,7 @@
 """Grouped products (gemm_grouped_run) on the GPU against plain 64-bit
 products, group by group, for every kernel family that takes the sizes."""
+import os
+
 import pytest
 import torch
 
@@ -9,11 +11,20 @@ from sparse_tiled_gemm_amd import gemm as G
 
 pytestmark = pytest.mark.gpu
 
-FAMILIES = ["auto", "generic", "skinny", "tiled128", "tiled256"]
+FAMILIES = ["auto", "generic", "skinny", "tiled128", "tiled128x256", "tiled256"]
 
 
 def _plan(algo, *a, **kw):
     """A plan, or a skip where the forced family does not take the sizes."""
+    if algo == "tiled128x256":  # (no algo code of its own: the tuning override)
+        os.environ["STGEMM_FORCE_KERNEL"] = algo
+        try:
+            plan = G.gemm_grouped_plan(G.make_grouped_desc(*a, **kw))
+        finally:
+            del os.environ["STGEMM_FORCE_KERNEL"]
+        if algo not in plan.name:
+            pytest.skip("%s does not take these sizes" % algo)
+        return plan
     try:
         return G.gemm_grouped_plan(G.make_grouped_desc(*a, algo=algo, **kw))
     except G.GemmError as e:
@@ -86,6 +97,29 @@ def test_rows(case, b_layout, algo):
         wv[a:a + n, :N] = D[a:a + n]
     it = torch.int32 if d_type == "f32" else torch.int16
     assert torch.equal(d_buf.view(it), want.view(it))  # nothing else is written
+
+
+@pytest.mark.parametrize("counts,N", [([700, 1, 300, 0, 255], 264), ([512] * 8, 4096),
+                                      ([256 * 16 + 3, 5000], 4100)])
+def test_last_round(counts, N):
+    """The 256 x 256 tiles past the last full round of compute units go in
+    halves: fewer tiles than one round, exactly one, some more."""
+    say("last round", counts, N)
+    gen = torch.Generator().manual_seed(N)
+    offsets, K = _bounds(counts), 72
+    rows = offsets[-1]
+    plan = _plan("tiled256", "rows", rows, N, K, len(counts), "bf16", "bf16", "f32")
+    A, _ = _mat(gen, rows, K, "bf16")
+    B, _ = _mat(gen, len(counts) * N, K, "bf16", 0, K ** -0.5)
+    D = torch.full((rows, N), float("nan"), device="cuda")
+    G.gemm_grouped_run(plan, A, B, None, torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+                       None, D)
+    torch.cuda.synchronize()
+    d = D.cpu()
+    for a, ref, S in R.rows_ref(A.cpu(), B.cpu().reshape(len(counts), N, K), offsets,
+                                "col").values():
+        err = (d[a:a + len(ref)].double() - ref).abs()
+        assert (err <= R.half_step("f32", ref) + (K + 2) * 2 * R.U32 * S).all()
 
 
 @pytest.mark.parametrize("offsets", [[0, 40, 20, 60], [-7, 10, 1000, 64], [64, 64, 64, 0],
