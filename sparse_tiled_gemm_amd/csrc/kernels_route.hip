@@ -188,91 +188,71 @@ __global__ __launch_bounds__(SORT_NT) void k_route_place(RouteArgs a)
 
 // ---------------------------------------------------------------- rows
 
-// Up to ROUTE_SMALL slots: every workgroup sorts them all for itself (4
-// steps of 64 slots per wave at most) and copies its share of the tokens, so
-// that a decoder's few tokens need one launch; workgroup 0 writes the lists.
-// COPY: with the rows (dispatch).
-constexpr int SMALL_NT = 256, SMALL_W = SMALL_NT / 64;
+// Up to ROUTE_SMALL slots, one launch: a workgroup counts all slots by group
+// for itself (those before its own apart), ranks its own ROUTE_CHUNK slots
+// and, with COPY (dispatch), moves their rows.  blockIdx.y cuts the columns, so
+// that a decoder's few tokens still spread over the chip; workgroups of y = 0
+// write the lists.  With gemm_moe_combine behind it, against the three
+// launches of the chunked sort and copy: 680 tokens of 3 choices, 13 groups,
+// 1027 columns 11.4 and 17.8 us, 1360 tokens 17.8 and 18.2 us, 1999 tokens
+// 24.8 and 20.0 us.
+constexpr int ROUTE_CHUNK = 32;
 template <bool COPY>
-__global__ __launch_bounds__(SMALL_NT) void k_route_small(RouteArgs a, RowsArgs r, int pieces)
+__global__ __launch_bounds__(SORT_NT) void k_route_small(RouteArgs a, RowsArgs r, int pieces)
 {
-    __shared__ int tot[ROUTE_MAX_GROUPS + 1];
-    __shared__ int whist[SMALL_W][ROUTE_MAX_GROUPS];
-    __shared__ int place[ROUTE_SMALL];
-    __shared__ int tmp[SMALL_W];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int G = a.groups, n = (int)a.slots;
-    const int per = ((n + SMALL_NT - 1) / SMALL_NT) * 64; // slots per wave: 64 .. 256
-    int gid[ROUTE_SMALL / SMALL_NT];
+    __shared__ int tot[ROUTE_MAX_GROUPS + 1], bef[ROUTE_MAX_GROUPS];
+    __shared__ int place[ROUTE_CHUNK];
+    __shared__ int tmp[SORT_W];
+    constexpr int PER = ROUTE_SMALL / SORT_NT; // slots per thread at most
+    const int tid = threadIdx.x;
+    const int G = a.groups, n = (int)a.slots, c0 = blockIdx.x * ROUTE_CHUNK;
+    int gid[PER];
 #pragma unroll
-    for (int i = 0; i < ROUTE_SMALL / SMALL_NT; ++i) {
-        const int s = wave * per + 64 * i + lane;
-        gid[i] = 64 * i < per && s < n ? route_id(a, s) : -1;
-    }
-    for (int g = tid; g < G; g += SMALL_NT)
-#pragma unroll
-        for (int w = 0; w < SMALL_W; ++w)
-            whist[w][g] = 0;
+    for (int i = 0; i < PER; ++i)
+        gid[i] = i * SORT_NT + tid < n ? route_id(a, i * SORT_NT + tid) : -1;
+    // the first wave's lanes hold this workgroup's slots
+    const int own = c0 + tid;
+    const int g = tid < ROUTE_CHUNK && own < n ? route_id(a, own) : -1;
+    for (int i = tid; i < G; i += SORT_NT)
+        tot[i] = bef[i] = 0;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < ROUTE_SMALL / SMALL_NT; ++i)
-        if (gid[i] >= 0)
-            atomicAdd(&whist[wave][gid[i]], 1);
-    __syncthreads();
-    for (int g = tid; g < G; g += SMALL_NT) {
-        int t = 0;
-#pragma unroll
-        for (int w = 0; w < SMALL_W; ++w) {
-            const int v = whist[w][g];
-            whist[w][g] = t;
-            t += v;
+    for (int i = 0; i < PER; ++i)
+        if (gid[i] >= 0) {
+            atomicAdd(&tot[gid[i]], 1);
+            if (i * SORT_NT + tid < c0)
+                atomicAdd(&bef[gid[i]], 1);
         }
-        tot[g] = t;
-    }
     __syncthreads();
-    scan_lds<SMALL_NT>(tot, G, tmp, tid);
-    const int bits = 32 - __builtin_clz(G);
-#pragma unroll
-    for (int i = 0; i < ROUTE_SMALL / SMALL_NT; ++i) {
-        if (64 * i >= per)
-            break; // (uniform)
-        const int s = wave * per + 64 * i + lane, g = gid[i];
-        const uint64_t same = same_group(g, bits);
-        const int rank = lanes_below(same);
-        int p = -1, c = 0;
-        if (g >= 0) {
-            c = whist[wave][g] + rank;
-            p = tot[g] + c;
-        }
-        wave_lds_sync();
-        if (g >= 0 && rank == 0)
-            whist[wave][g] = c + __popcll(same);
-        wave_lds_sync();
-        if (s < n)
-            place[s] = p;
-    }
-    __syncthreads();
-    if (blockIdx.x == 0) {
-        for (int g = tid; g <= G; g += SMALL_NT)
-            a.offsets[g] = tot[g];
-        for (int s = tid; s < n; s += SMALL_NT) {
-            const int p = place[s];
-            a.pos[s] = p;
-            if (p >= 0)
-                a.order[p] = s;
-            if (s >= tot[G])
-                a.order[s] = -1;
+    scan_lds<SORT_NT>(tot, G, tmp, tid);
+    if (tid < 64) {
+        const int rank = lanes_below(same_group(g, 32 - __builtin_clz(G)));
+        const int p = g >= 0 ? tot[g] + bef[g] + rank : -1;
+        if (tid < ROUTE_CHUNK && own < n) {
+            place[tid] = p;
+            if (blockIdx.y == 0) {
+                a.pos[own] = p;
+                if (p >= 0)
+                    a.order[p] = own;
+                if (own >= tot[G])
+                    a.order[own] = -1;
+            }
         }
     }
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = tid; i <= G; i += SORT_NT)
+            a.offsets[i] = tot[i];
     if constexpr (COPY) {
-        // pieces of 8 columns of every (token, choice), over all workgroups
-        const int total = n * pieces; // n <= 1024, pieces <= 2^20 (host)
-        for (int i = blockIdx.x * SMALL_NT + tid; i < total; i += gridDim.x * SMALL_NT) {
-            const int s = i / pieces;
-            const int64_t c = (int64_t)(i - s * pieces) * 8;
+        __syncthreads();
+        // this workgroup's pieces of 8 columns of its slots
+        const int per = (pieces + gridDim.y - 1) / gridDim.y, p0 = blockIdx.y * per;
+        const int np = min(per, pieces - p0), total = np > 0 ? min(ROUTE_CHUNK, n - c0) * np : 0;
+        for (int i = tid; i < total; i += SORT_NT) {
+            const int s = i / np;
+            const int64_t c = (int64_t)(p0 + i - s * np) * 8;
             const int p = place[s];
             if (p >= 0) {
-                const int64_t t = s / (int)r.topk;
+                const int64_t t = (c0 + s) / (int)r.topk;
                 const int nc = (int)min((int64_t)8, r.cols - c);
                 store8((uint16_t *)r.out + p * r.ld_out + c,
                        load8((const uint16_t *)r.in + t * r.ld_in + c, nc), nc);
@@ -302,45 +282,49 @@ __global__ __launch_bounds__(256) void k_route_copy(RowsArgs r)
     }
 }
 
-// Y[t] = sum over k of w[t,k] Ys[pos[t,k]].  TPR lanes per token; four rows
-// are in flight per lane.
-template <bool BF, int TPR>
+// Y[t] = sum over k of w[t,k] Ys[pos[t,k]].  TPR lanes per token and
+// blockIdx.y's part of the columns, one piece per lane; KB rows are in flight
+// per lane.
+template <bool BF, int TPR, int KB>
 __global__ __launch_bounds__(256) void k_combine(RowsArgs r)
 {
+    const int64_t c = ((int64_t)blockIdx.y * TPR + threadIdx.x % TPR) * 8;
+    if (c >= r.cols)
+        return;
+    const int n = (int)min((int64_t)8, r.cols - c);
     int64_t t = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
     for (; t < r.tokens; t += (int64_t)gridDim.x * (256 / TPR)) {
-    const int32_t *pos = r.pos + t * r.topk;
-    const float *wt = r.weights ? r.weights + t * r.topk : nullptr;
-    uint16_t *y = (uint16_t *)r.out + t * r.ld_out;
-    for (int64_t c = (threadIdx.x % TPR) * 8; c < r.cols; c += TPR * 8) {
-        const int n = (int)min((int64_t)8, r.cols - c);
+        const int32_t *pos = r.pos + t * r.topk;
+        const float *wt = r.weights ? r.weights + t * r.topk : nullptr;
         float acc[8] = {};
-        for (int64_t k0 = 0; k0 < r.topk; k0 += 4) {
-            u4_t v[4];
-            float w[4];
+        for (int64_t k0 = 0; k0 < r.topk; k0 += KB) {
+            int64_t p[KB];
+            u4_t v[KB];
+            float w[KB];
+            // (a slot without a place adds nothing, whatever its weight)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t k = k0 + q;
-                const int64_t p = k < r.topk ? pos[k] : -1;
-                const bool have = p >= 0 && p < r.rows;
-                v[q] = u4_t{};
-                w[q] = 0.0f; // a slot without a place adds nothing, whatever its weight
-                if (have) {
-                    v[q] = load8((const uint16_t *)r.in + p * r.ld_in + c, n);
-                    w[q] = wt ? wt[k] : 1.0f;
-                }
+            for (int q = 0; q < KB; ++q) {
+                p[q] = k0 + q < r.topk ? pos[k0 + q] : -1;
+                p[q] = p[q] < r.rows ? p[q] : -1;
+                w[q] = wt && k0 + q < r.topk ? wt[k0 + q] : 1.0f;
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < KB; ++q) {
+                v[q] = u4_t{};
+                if (p[q] >= 0)
+                    v[q] = load8((const uint16_t *)r.in + p[q] * r.ld_in + c, n);
+            }
+#pragma unroll
+            for (int q = 0; q < KB; ++q) {
                 float f[8];
                 widen8<BF>(v[q], f);
+                const float x = p[q] >= 0 ? w[q] : 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    acc[e] = __builtin_fmaf(w[q], f[e], acc[e]);
+                    acc[e] = __builtin_fmaf(x, f[e], acc[e]);
             }
         }
-        store8(y + c, narrow8<BF>(acc), n);
-    }
+        store8((uint16_t *)r.out + t * r.ld_out + c, narrow8<BF>(acc), n);
     }
 }
 
@@ -426,11 +410,11 @@ __global__ __launch_bounds__(256) void k_combine_backward(RowsArgs r)
 
 // ---------------------------------------------------------------- launch
 
-// Workgroups for n tokens, `per` of them each; past 2^20 they take several.
+// Workgroups for n tokens, `per` of them each; past 2^18 they take several.
 static unsigned blocks(int64_t n, int per)
 {
     const int64_t b = (n + per - 1) / per;
-    return (unsigned)(b < (1 << 20) ? b : (1 << 20));
+    return (unsigned)(b < (1 << 18) ? b : (1 << 18));
 }
 
 // Lanes per row of 8-column pieces: enough for one pass over a narrow row,
@@ -443,13 +427,18 @@ static int lanes_per_row(int64_t cols)
 hipError_t launch_route(const RouteArgs &a, const RowsArgs *r, hipStream_t s)
 {
     if (a.slots <= ROUTE_SMALL) {
+        const unsigned chunks = (unsigned)(a.slots > 0 ? (a.slots + ROUTE_CHUNK - 1) / ROUTE_CHUNK : 1);
         if (!r) {
-            hipLaunchKernelGGL(k_route_small<false>, dim3(1), dim3(SMALL_NT), 0, s, a, RowsArgs{}, 0);
+            hipLaunchKernelGGL(k_route_small<false>, dim3(chunks), dim3(SORT_NT), 0, s, a, RowsArgs{},
+                               0);
         } else {
-            const int64_t pieces = (r->cols + 7) / 8;
-            const int64_t nb = (a.slots * pieces + SMALL_NT - 1) / SMALL_NT;
-            hipLaunchKernelGGL(k_route_small<true>, dim3((unsigned)(nb < 1 ? 1 : nb < 512 ? nb : 512)),
-                               dim3(SMALL_NT), 0, s, a, *r, (int)pieces);
+            // about two workgroups per compute unit, each with work for its lanes
+            const int64_t pieces = (r->cols + 7) / 8, slots = a.slots < ROUTE_CHUNK ? a.slots : ROUTE_CHUNK;
+            int64_t y = (slots * pieces + SORT_NT - 1) / SORT_NT;
+            if (y > 512 / (int64_t)chunks)
+                y = 512 / (int64_t)chunks;
+            hipLaunchKernelGGL(k_route_small<true>, dim3(chunks, (unsigned)(y < 1 ? 1 : y)),
+                               dim3(SORT_NT), 0, s, a, *r, (int)pieces);
         }
         return hipGetLastError();
     }
@@ -470,24 +459,30 @@ hipError_t launch_route(const RouteArgs &a, const RowsArgs *r, hipStream_t s)
     return hipGetLastError();
 }
 
-template <bool BF>
+template <bool BF, int TPR>
 static void combine_t(const RowsArgs &a, hipStream_t s)
 {
+    // (cols <= 2^23: at most 2^12 column parts of 256 lanes x 8)
+    const dim3 grid(blocks(a.tokens, 256 / TPR), (unsigned)((a.cols + 8 * TPR - 1) / (8 * TPR)));
+    if (a.topk <= 4)
+        hipLaunchKernelGGL((k_combine<BF, TPR, 4>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_combine<BF, TPR, 8>), grid, dim3(256), 0, s, a);
+}
+
+template <bool BF>
+static void combine_lanes(const RowsArgs &a, hipStream_t s)
+{
     switch (lanes_per_row(a.cols)) {
-    case 16:
-        hipLaunchKernelGGL((k_combine<BF, 16>), dim3(blocks(a.tokens, 16)), dim3(256), 0, s, a);
-        break;
-    case 64:
-        hipLaunchKernelGGL((k_combine<BF, 64>), dim3(blocks(a.tokens, 4)), dim3(256), 0, s, a);
-        break;
-    default:
-        hipLaunchKernelGGL((k_combine<BF, 256>), dim3(blocks(a.tokens, 1)), dim3(256), 0, s, a);
+    case 16: combine_t<BF, 16>(a, s); break;
+    case 64: combine_t<BF, 64>(a, s); break;
+    default: combine_t<BF, 256>(a, s);
     }
 }
 
 hipError_t launch_combine(const RowsArgs &a, hipStream_t s)
 {
-    a.bf16 ? combine_t<true>(a, s) : combine_t<false>(a, s);
+    a.bf16 ? combine_lanes<true>(a, s) : combine_lanes<false>(a, s);
     return hipGetLastError();
 }
 

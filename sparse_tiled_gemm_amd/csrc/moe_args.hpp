@@ -11,9 +11,9 @@ namespace stg {
 // ---------------------------------------------------------------- routing
 
 constexpr int ROUTE_MAX_GROUPS = 1024;
-// up to this many slots every workgroup sorts all of them for itself in one
+// up to this many slots every workgroup counts all of them for itself, in one
 // launch; more are sorted in chunks by two launches
-constexpr int ROUTE_SMALL = 1024;
+constexpr int ROUTE_SMALL = 4096;
 
 struct RouteArgs {
     int64_t tokens, topk, slots;

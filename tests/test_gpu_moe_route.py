@@ -37,7 +37,8 @@ def _sort(ids, groups):
 @pytest.mark.parametrize("tokens,topk,groups,drop,id_bytes", [
     (1, 1, 1, 0.0, 4), (1, 8, 64, 0.0, 8), (0, 2, 5, 0.0, 8), (63, 1, 3, 0.2, 4),
     (64, 4, 7, 0.0, 8), (257, 3, 13, 0.1, 4), (512, 2, 1024, 0.0, 8),    # one launch
-    (513, 2, 1000, 0.3, 8), (1025, 1, 1, 0.5, 4), (4096, 8, 256, 0.05, 8),  # chunked
+    (513, 2, 1000, 0.3, 8), (1025, 1, 1, 0.5, 4), (4096, 1, 31, 0.1, 8),
+    (4097, 1, 31, 0.1, 8), (4096, 8, 256, 0.05, 8), (5000, 2, 1024, 0.0, 4),  # chunked
     (1999, 3, 13, 1.0, 8), (40000, 8, 65, 0.01, 4),
 ])
 def test_sort(tokens, topk, groups, drop, id_bytes):
@@ -69,6 +70,7 @@ CASES = [  # tokens, topk, groups, cols, dtype, drop, ld extra, element offset
     (3, 2, 4, 7, "bf16", 0.0, 2, 1), (100, 2, 8, 128, "f16", 0.2, 8, 8),
     (129, 3, 5, 1027, "f16", 0.1, 0, 0), (700, 5, 9, 515, "bf16", 0.3, 3, 1),
     (2100, 1, 16, 72, "bf16", 0.0, 0, 0), (2049, 6, 30, 24, "f16", 0.5, 0, 3),
+    (2800, 3, 20, 520, "f16", 0.1, 0, 0), (4200, 2, 11, 40, "bf16", 0.0, 0, 0),
     (300, 9, 12, 2056, "bf16", 0.1, 0, 0), (50, 4, 6, 64, "f16", 1.0, 0, 0),
 ]
 

@@ -44,7 +44,7 @@ ROUTE = dict(tokens=8, topk=2, groups=4, cols=64, dtype="bf16", ids=P(0), X=P(1)
     (dict(order=None), G.GEMM_ERR_NULL_POINTER),
     (dict(pos=None), G.GEMM_ERR_NULL_POINTER),
     (dict(Xs=None), G.GEMM_ERR_NULL_POINTER),
-    (dict(tokens=1024, workspace=None), G.GEMM_ERR_NULL_POINTER),
+    (dict(tokens=4096, workspace=None), G.GEMM_ERR_NULL_POINTER),
     (dict(ids=P(0, 4)), G.GEMM_ERR_MISALIGNED),
     (dict(X=P(1, 1)), G.GEMM_ERR_MISALIGNED),
     (dict(pos=P(4, 2)), G.GEMM_ERR_MISALIGNED),
@@ -60,8 +60,8 @@ def test_dispatch_refusals(change, status):
 
 def test_sort_workspace():
     assert G.gemm_moe_sort_workspace(0, 1, 1) == 0
-    assert G.gemm_moe_sort_workspace(1024, 1, 64) == 0
-    assert G.gemm_moe_sort_workspace(1025, 1, 64) == 2 * 64 * 4
+    assert G.gemm_moe_sort_workspace(4096, 1, 64) == 0
+    assert G.gemm_moe_sort_workspace(4097, 1, 64) == 5 * 64 * 4
     # at most 256 chunks
     assert G.gemm_moe_sort_workspace(1 << 20, 8, 1024) <= 256 * 1024 * 4
     for bad in [(-1, 1, 1), (1, 0, 1), (1, 1, 0), (1 << 30, 4, 1), (1, 1, 1025)]:
