@@ -22,8 +22,6 @@ static hipError_t launch_op(int family, const GroupedArgs &a, hipStream_t s)
 {
     if (family == GF_TILED_256)
         return a.b_row ? launch_t<OP, GL_MN, 256, 256>(a, s) : launch_t<OP, GL_K, 256, 256>(a, s);
-    if (family == GF_TILED_128X256)
-        return a.b_row ? launch_t<OP, GL_MN, 128, 256>(a, s) : launch_t<OP, GL_K, 128, 256>(a, s);
     return a.b_row ? launch_t<OP, GL_MN, 128, 128>(a, s) : launch_t<OP, GL_K, 128, 128>(a, s);
 }
 

@@ -21,8 +21,6 @@ static hipError_t launch_op(int family, const GroupedArgs &a, hipStream_t s)
 {
     if (family == GF_TILED_256)
         return a.bs ? launch_t<OP, GL_Q8, 256, 256>(a, s) : launch_t<OP, GL_MN, 256, 256>(a, s);
-    if (family == GF_TILED_128X256)
-        return a.bs ? launch_t<OP, GL_Q8, 128, 256>(a, s) : launch_t<OP, GL_MN, 128, 256>(a, s);
     return a.bs ? launch_t<OP, GL_Q8, 128, 128>(a, s) : launch_t<OP, GL_MN, 128, 128>(a, s);
 }
 

@@ -372,8 +372,7 @@ static bool grouped_tiled_ok(const gemm_grouped_desc_t &d)
 
 static const char *grouped_family_name(int f)
 {
-    static const char *const n[GF_COUNT] = {"generic", "skinny", "tiled128", "tiled128x256",
-                                             "tiled256"};
+    static const char *const n[GF_COUNT] = {"generic", "skinny", "tiled128", "tiled256"};
     return n[f];
 }
 
@@ -389,7 +388,20 @@ gemm_status_t gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_pl
     DeviceInfo di;
     CHECK(check_device(&dev, &di));
     const bool tiled = grouped_tiled_ok(d);
-    const int auto_tiled = d.rows >= 192 * (int64_t)d.groups ? GF_TILED_256 : GF_TILED_128;
+    // 256- against 128-wide tiles, us on MI355X.  Rows: once the expected
+    // 128-wide tiles (half a tile per group wasted) no longer fit one per
+    // compute unit, and from about 32 rows per group (8 groups, K 1024: 512 x
+    // 2048 17 and 13, 2048 x 2048 20 and 19, 8192 x 2048 47 and 52; 32 groups
+    // of 16 rows, 4096 x 2048 140 and 125).  Weights: once the 128-wide ones,
+    // two per compute unit, no longer fit at once (4 groups of 2048 rows, 2048
+    // x 1024 75 and 57, 2048 x 4096 144 and 199; 32 groups of 256 rows, 512 x
+    // 256 35 and 20, 512 x 4096 82 and 98).
+    const int64_t tiles_n = ceil_div(d.N, 128);
+    const bool small = d.mode == GEMM_GROUPED_WEIGHTS
+                           ? d.groups * ceil_div(d.K, 128) * tiles_n <= 2 * di.num_cu
+                           : d.rows < 32 * (int64_t)d.groups ||
+                                 (d.rows / 128 + d.groups / 2) * tiles_n <= di.num_cu;
+    const int auto_tiled = small ? GF_TILED_128 : GF_TILED_256;
     // Few rows per group: B's stream bounds the product (the plan cannot see
     // the groups' bounds; every family serves groups of any length).  With B
     // 32 x 4096 x 2048 the skinny kernel and the 128 x 128 tile took 109 and
@@ -411,12 +423,6 @@ gemm_status_t gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_pl
     case GEMM_ALGO_TILED_128: fam = tiled ? GF_TILED_128 : -1; break;
     case GEMM_ALGO_TILED_256: fam = tiled ? GF_TILED_256 : -1; break;
     default: fam = -1;
-    }
-    if (const char *force = getenv("STGEMM_FORCE_KERNEL")) { // tuning override
-        for (int f = GF_GENERIC; f < GF_COUNT; ++f)
-            if (strcmp(force, grouped_family_name(f)) == 0 &&
-                (f == GF_GENERIC || (f == GF_SKINNY ? skinny : tiled)))
-                fam = f;
     }
     if (fam < 0)
         return fail(GEMM_ERR_UNSUPPORTED, "requested algorithm cannot serve this problem");

@@ -70,10 +70,9 @@ hipError_t launch_swiglu_backward(const Q8Args &a, hipStream_t s);
 
 enum GroupedFamily {
     GF_GENERIC = 0,
-    GF_SKINNY,
-    GF_TILED_128,    // 128 x 128, two workgroups per compute unit
-    GF_TILED_128X256,
-    GF_TILED_256,
+    GF_SKINNY,    // rows: few per group
+    GF_TILED_128, // 128 x 128 tiles, two workgroups per compute unit
+    GF_TILED_256, // 256 x 256 tiles, one
     GF_COUNT
 };
 

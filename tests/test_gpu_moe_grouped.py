@@ -1,7 +1,5 @@
 """Grouped products (gemm_grouped_run) on the GPU against plain 64-bit
 products, group by group, for every kernel family that takes the sizes."""
-import os
-
 import pytest
 import torch
 
@@ -11,20 +9,11 @@ from sparse_tiled_gemm_amd import gemm as G
 
 pytestmark = pytest.mark.gpu
 
-FAMILIES = ["auto", "generic", "skinny", "tiled128", "tiled128x256", "tiled256"]
+FAMILIES = ["auto", "generic", "skinny", "tiled128", "tiled256"]
 
 
 def _plan(algo, *a, **kw):
     """A plan, or a skip where the forced family does not take the sizes."""
-    if algo == "tiled128x256":  # (no algo code of its own: the tuning override)
-        os.environ["STGEMM_FORCE_KERNEL"] = algo
-        try:
-            plan = G.gemm_grouped_plan(G.make_grouped_desc(*a, **kw))
-        finally:
-            del os.environ["STGEMM_FORCE_KERNEL"]
-        if algo not in plan.name:
-            pytest.skip("%s does not take these sizes" % algo)
-        return plan
     try:
         return G.gemm_grouped_plan(G.make_grouped_desc(*a, algo=algo, **kw))
     except G.GemmError as e:
