@@ -721,16 +721,16 @@ __device__ STG_AI inline f4_t epi_affine(const EpiArgs &e, f4_t t, f4_t b)
 constexpr int EPI_CPOL = 2; // the NT bit of the buffer instructions' cache-policy operand
 
 // Store four finished values at byte offset voff + soff of the D resource.
-template <int KIND>
+template <int KIND, int CPOL>
 __device__ STG_AI inline void epi_store4(__amdgpu_buffer_rsrc_t rd, int voff, int soff, f4_t y)
 {
     if constexpr (KIND == OUT_F32) {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4_t, y), rd, voff, soff, EPI_CPOL);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4_t, y), rd, voff, soff, CPOL);
     } else if constexpr (KIND == OUT_E4M3 || KIND == OUT_E5M2) {
         constexpr bool E4 = KIND == OUT_E4M3;
         const uint32_t w = f32_to_fp8_bits<E4>(y[0]) | (f32_to_fp8_bits<E4>(y[1]) << 8) |
                            (f32_to_fp8_bits<E4>(y[2]) << 16) | (f32_to_fp8_bits<E4>(y[3]) << 24);
-        __builtin_amdgcn_raw_buffer_store_b32(w, rd, voff, soff, EPI_CPOL);
+        __builtin_amdgcn_raw_buffer_store_b32(w, rd, voff, soff, CPOL);
     } else {
         typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
         u2_t w;
@@ -741,7 +741,7 @@ __device__ STG_AI inline void epi_store4(__amdgpu_buffer_rsrc_t rd, int voff, in
             w[0] = f32_to_bf16_bits(y[0]) | ((uint32_t)f32_to_bf16_bits(y[1]) << 16);
             w[1] = f32_to_bf16_bits(y[2]) | ((uint32_t)f32_to_bf16_bits(y[3]) << 16);
         }
-        __builtin_amdgcn_raw_buffer_store_b64(w, rd, voff, soff, EPI_CPOL);
+        __builtin_amdgcn_raw_buffer_store_b64(w, rd, voff, soff, CPOL);
     }
 }
 
@@ -791,7 +791,8 @@ __device__ STG_AI inline i4_t add_c(i4_t v, i4_t c, int sat)
 // once per slab).  Other blocks take an element-by-element path.
 // KIND: the output kind (OUT_S32: int32 output of an integer accumulator;
 // a float kind takes integer accumulators' values, RNE to fp32, first).
-template <class OP, int FM, int FN, int KIND>
+// CPOL: the cache policy of C's loads and D's stores.
+template <class OP, int FM, int FN, int KIND, int CPOL = EPI_CPOL>
 __device__ STG_AI inline void epilogue_slabs(const EpiArgs &e, typename OP::acc_t (&acc)[FM][FN],
                                       int64_t m0, int64_t n0, int lane, uint32_t *lds_wave)
 {
@@ -851,12 +852,12 @@ __device__ STG_AI inline void epilogue_slabs(const EpiArgs &e, typename OP::acc_
                 if (IOUT || e.c_kind == 0) {
                     cv[p] = __builtin_bit_cast(
                         u4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                  rc, vc, (32 * i + p * RPP) * ldc_b, EPI_CPOL));
+                                  rc, vc, (32 * i + p * RPP) * ldc_b, CPOL));
                 } else {
                     typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
                     const u2_t h = __builtin_bit_cast(
                         u2_t, __builtin_amdgcn_raw_buffer_load_b64(
-                                  rc, vc, (32 * i + p * RPP) * ldc_b, EPI_CPOL));
+                                  rc, vc, (32 * i + p * RPP) * ldc_b, CPOL));
                     cv[p] = u4_t{h.x, h.y, 0u, 0u};
                 }
             }
@@ -901,10 +902,10 @@ __device__ STG_AI inline void epilogue_slabs(const EpiArgs &e, typename OP::acc_
                 if constexpr (IOUT) {
                     const v4_t w = has_c ? add_c(v, __builtin_bit_cast(v4_t, cv[p]), e.sat) : v;
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4_t, w), rd, vd, soff,
-                                                           EPI_CPOL);
+                                                           CPOL);
                 } else {
                     const f4_t f = has_c ? add_c(v, widen_c(cv[p], e.c_kind)) : v;
-                    epi_store4<KIND>(rd, vd, soff, epi_affine(e, f, bv));
+                    epi_store4<KIND, CPOL>(rd, vd, soff, epi_affine(e, f, bv));
                 }
             }
         } else {

@@ -68,20 +68,22 @@ __device__ STG_AI inline void tile_of(int t, int tiles_m, int tiles_n, int &tm, 
 // Region row i of half h is tile row at(h, i): K-contiguous operands give each
 // wave neighbouring halves, so that its block of the output is one piece; an
 // MN-major region is a contiguous run, whose K rows are then fetched in 2 R
-// bytes at a time.
-template <int LAYOUT, int R, int PIECE, bool BF>
+// bytes at a time.  SETS: register sets of an 8-bit operand; NW: waves that
+// copy; HALVES: 1 for a tile whose operand is one region.
+template <int LAYOUT, int R, int PIECE, bool BF, int SETS = 1, int NW = 8, int HALVES = 2>
 struct Operand {
     static constexpr bool KC = LAYOUT == GL_K;
-    static constexpr int LD = R * 128 / 8192;       // 1 KB copies per wave and region
+    static constexpr int LD = R * 128 / (NW * 1024); // 1 KB copies per wave and region
     static constexpr int VM = LAYOUT == GL_Q8 ? 2 * LD : LD; // vector-memory instructions
     static constexpr int PITCH = R * 2;             // MN-major: bytes of a K row
     static constexpr int CPR = PITCH / 16;          // its 16-byte chunks
     static constexpr int FR = PIECE / 16;           // fragments of a wave
+    static constexpr int ROWS = PIECE;
     static_assert(LD >= 1, "a region is at least one copy per wave");
 
     __device__ STG_AI static int at(int h, int i)
     {
-        return KC ? (i / PIECE) * 2 * PIECE + h * PIECE + i % PIECE : h * R + i;
+        return KC && HALVES == 2 ? (i / PIECE) * 2 * PIECE + h * PIECE + i % PIECE : h * R + i;
     }
 
     // (a transposing read touches K rows 8 q + 4 t + 0..3, q = 0, 1 in one
@@ -97,26 +99,26 @@ struct Operand {
     int64_t span;        // K-contiguous: rows that exist; MN-major: bytes of a K row that exist
     const uint8_t *sc;   // GL_Q8: scales of the first K row, at the tile's first column's block
     int64_t ld_sc;
-    int voff[2][LD];     // [half][copy]: byte offset of this lane in the tile
-    int soff8[2][LD];    // GL_Q8: offset of its scale
+    int voff[HALVES][LD]; // [half][copy]: byte offset of this lane in the tile
+    int soff8[HALVES][LD]; // GL_Q8: offset of its scale
     int kc;              // K-contiguous: byte in the K tile of this lane's chunk
     int rd[FR > 2 ? FR : 2]; // read offsets (K-contiguous: one per K step; else per fragment)
-    uint32_t code[2][LD][2], sbyte[2][LD]; // GL_Q8: in flight, by half
+    uint32_t code[SETS][HALVES][LD][2], sbyte[SETS][HALVES][LD]; // GL_Q8: in flight, by half
 
     // wave_u: the wave's number; part: its place along this operand
     __device__ STG_AI void init(int lane, int wave_u, int part)
     {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < HALVES; ++h)
 #pragma unroll
             for (int j = 0; j < LD; ++j) {
                 if constexpr (KC) {
-                    const int i = j * 64 + wave_u * 8 + (lane >> 3);
+                    const int i = (j * NW + wave_u) * 8 + (lane >> 3);
                     const int row = at(h, i);
                     kc = ((lane & 7) ^ ((lane >> 3) & 7)) * 16;
                     voff[h][j] = row * (int)ld + kc;
                 } else {
-                    const int c = (j * 8 + wave_u) * 64 + lane; // chunk of the region
+                    const int c = (j * NW + wave_u) * 64 + lane; // chunk of the region
                     const int k = c / CPR;
                     const int i = ((c % CPR) ^ (mn_swz(k) << 1)) * 8; // region column
                     const int col = at(h, i);
@@ -142,7 +144,8 @@ struct Operand {
         }
     }
 
-    // Copy half h of K tile kt into `region` (LDS).
+    // Copy half h of K tile kt into `region` (LDS); GL_Q8: into register set Q.
+    template <int Q = 0>
     __device__ STG_AI void copy(uint8_t *region, auto half, int kt, int wave_u)
     {
         constexpr int h = decltype(half)::value;
@@ -152,7 +155,7 @@ struct Operand {
             const bool in = kt * 128 + kc < k_bytes;
 #pragma unroll
             for (int j = 0; j < LD; ++j)
-                dma16(r, region + (j * 8 + wave_u) * 1024, in ? voff[h][j] : (int)0x80000000,
+                dma16(r, region + (j * NW + wave_u) * 1024, in ? voff[h][j] : (int)0x80000000,
                       kt * 128);
         } else {
             // the tile's K rows start the resource, so that every offset fits
@@ -163,7 +166,7 @@ struct Operand {
             if constexpr (LAYOUT == GL_MN) {
 #pragma unroll
                 for (int j = 0; j < LD; ++j)
-                    dma16(r, region + (j * 8 + wave_u) * 1024, voff[h][j], 0);
+                    dma16(r, region + (j * NW + wave_u) * 1024, voff[h][j], 0);
             } else {
                 const __amdgpu_buffer_rsrc_t rs = epi_rsrc(
                     sc + (int64_t)kt * 64 * ld_sc, left > 0 ? (left - 1) * ld_sc + (span + 31) / 32 : 0);
@@ -172,21 +175,22 @@ struct Operand {
                     typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
                     const u2_t c = __builtin_bit_cast(
                         u2_t, __builtin_amdgcn_raw_buffer_load_b64(r, voff[h][j], 0, 0));
-                    code[h][j][0] = c.x;
-                    code[h][j][1] = c.y;
-                    sbyte[h][j] = __builtin_amdgcn_raw_buffer_load_b8(rs, soff8[h][j], 0, 0);
+                    code[Q][h][j][0] = c.x;
+                    code[Q][h][j][1] = c.y;
+                    sbyte[Q][h][j] = __builtin_amdgcn_raw_buffer_load_b8(rs, soff8[h][j], 0, 0);
                 }
             }
         }
     }
 
-    // GL_Q8: half h's codes in registers, as 16-bit values into `region`.
+    // GL_Q8: half h's codes in register set Q, as 16-bit values into `region`.
+    template <int Q = 0>
     __device__ STG_AI void store(uint8_t *region, auto half, int lane, int wave_u)
     {
         constexpr int h = decltype(half)::value;
 #pragma unroll
         for (int j = 0; j < LD; ++j) {
-            const uint32_t sb = sbyte[h][j];
+            const uint32_t sb = sbyte[Q][h][j];
             u4_t v;
             // scales that cannot take a code past the type's range (448 *
             // 2^(sb - 127)), nor are NaN or subnormal: two values at a time
@@ -194,7 +198,7 @@ struct Operand {
                 const float s = __builtin_bit_cast(float, sb << 23);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    const int c = (int)code[h][j][w >> 1];
+                    const int c = (int)code[Q][h][j][w >> 1];
                     if constexpr (BF)
                         v[w] = __builtin_bit_cast(
                             uint32_t, w & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, true)
@@ -209,15 +213,15 @@ struct Operand {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     typedef float f2_t __attribute__((ext_vector_type(2)));
-                    const int c = (int)code[h][j][w >> 1];
+                    const int c = (int)code[Q][h][j][w >> 1];
                     const f2_t x = w & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(c, true)
                                          : __builtin_amdgcn_cvt_pk_f32_fp8(c, false);
-                    const float p = clamp16<BF>(x.x * s), q = clamp16<BF>(x.y * s);
-                    v[w] = BF ? f32_to_bf16_bits(p) | ((uint32_t)f32_to_bf16_bits(q) << 16)
-                              : f32_to_f16_bits(p) | ((uint32_t)f32_to_f16_bits(q) << 16);
+                    const float lo = clamp16<BF>(x.x * s), hi = clamp16<BF>(x.y * s);
+                    v[w] = BF ? f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16)
+                              : f32_to_f16_bits(lo) | ((uint32_t)f32_to_f16_bits(hi) << 16);
                 }
             }
-            *(u4_t *)(region + (j * 8 + wave_u) * 1024 + lane * 16) = v;
+            *(u4_t *)(region + (j * NW + wave_u) * 1024 + lane * 16) = v;
         }
     }
 
@@ -249,6 +253,133 @@ constexpr int region_bytes()
     return R * 128 > slab ? R * 128 : (slab + 1023) / 1024 * 1024;
 }
 
+// A tile's shape and operands: eight waves, 2 x 4, each operand in two halves.
+template <class OP, bool W_, int ALAY_, int BLAY_, int BM_, int BN_>
+struct TileShape {
+    static constexpr bool W = W_, BF = std::is_same<OP, Op16BF16>::value;
+    static constexpr int ALAY = ALAY_, BLAY = BLAY_, BM = BM_, BN = BN_;
+    static constexpr int GN = 4;                   // waves along N
+    static constexpr int WM = BM / 2, WN = BN / 4; // a wave's block
+    static constexpr int FM = WM / 16, FN = WN / 16;
+    static constexpr int FA = FM / 2, FB = FN / 2; // fragments of one of its halves
+    typedef Operand<ALAY, BM / 2, WM / 2, BF> OpA;
+    typedef Operand<BLAY, BN / 2, WN / 2, BF> OpB;
+    static constexpr int PA = OpA::KC ? 1 : 2, PB = OpB::KC ? 1 : 2; // pieces the block lies in
+};
+// The 64 x 64 tile: four waves, 2 x 2, each operand one region.
+template <class OP, bool W_, int ALAY_, int BLAY_>
+struct SmallShape {
+    static constexpr bool W = W_, BF = std::is_same<OP, Op16BF16>::value;
+    static constexpr int ALAY = ALAY_, BLAY = BLAY_, BM = 64, BN = 64;
+    static constexpr int GN = 2, WM = 32, WN = 32, FM = 2, FN = 2;
+    typedef Operand<ALAY, BM, WM, BF, 1, 4, 1> OpA;
+    typedef Operand<BLAY, BN, WN, BF, 2, 4, 1> OpB;
+    static constexpr int PA = 1, PB = 1;
+};
+
+// The operands of the tile of group t at (m_blk, n_blk); M, K: its group's
+// rows (of the output) and sum.
+template <class S>
+__device__ STG_AI inline void set_operands(typename S::OpA &A, typename S::OpB &B,
+                                           const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
+                                           int64_t n_blk, int64_t M, int64_t K, int lane, int wave)
+{
+    A.ld = a.lda * 2;
+    if constexpr (S::ALAY == GL_K) {
+        A.base = (const uint8_t *)a.A + (t.r0 + m_blk) * A.ld;
+        A.k_bytes = K * 2;
+        A.span = M - m_blk;
+    } else {
+        A.base = (const uint8_t *)a.A + t.r0 * A.ld + m_blk * 2;
+        A.k_bytes = K;
+        A.span = (M - m_blk) * 2;
+    }
+    constexpr int BE = S::BLAY == GL_Q8 ? 1 : 2;
+    B.ld = a.ldb * BE;
+    if constexpr (S::BLAY == GL_K) {
+        B.base = (const uint8_t *)a.B + ((int64_t)t.g * a.N + n_blk) * B.ld;
+        B.k_bytes = K * 2;
+        B.span = a.N - n_blk;
+    } else {
+        B.base = (const uint8_t *)a.B + (S::W ? t.r0 : (int64_t)t.g * a.K) * B.ld + n_blk * BE;
+        B.k_bytes = K;
+        B.span = (a.N - n_blk) * BE;
+    }
+    if constexpr (S::BLAY == GL_Q8) {
+        B.ld_sc = (a.N + 31) / 32;
+        B.sc = a.bs + t.r0 * B.ld_sc + n_blk / 32;
+    }
+    A.init(lane, wave, wave / S::GN);
+    B.init(lane, wave, wave % S::GN);
+}
+
+// Keeps a memory phase's steps in their order.
+__device__ STG_AI inline void in_order()
+{
+    STG_COMPILER_FENCE();
+    __builtin_amdgcn_sched_barrier(0);
+}
+// A workgroup barrier that nothing is moved across.
+__device__ STG_AI inline void tile_barrier()
+{
+    in_order();
+    __builtin_amdgcn_s_barrier();
+    in_order();
+}
+
+// A wave's accumulators to the output, through 32-row slabs in `lds`; in as
+// many pieces as its rows and columns lie in.
+template <class OP, class S>
+__device__ STG_AI inline void store_tile(const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
+                                         int64_t n_blk, int64_t M,
+                                         typename OP::acc_t (&acc)[S::FM][S::FN], int lane,
+                                         int wave, uint32_t *lds)
+{
+    typedef typename S::OpA OpA;
+    typedef typename S::OpB OpB;
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    EpiArgs e = group_epilogue(a, t.g, t.r0, M);
+    e.vec = a.vec;
+    constexpr int PA = S::PA, PB = S::PB;
+    auto store = [&](auto p, auto q, auto cpol) STG_AI {
+        constexpr int C = decltype(cpol)::value;
+        constexpr int FM = S::FM / PA, FN = S::FN / PB;
+        constexpr int I = decltype(p)::value * FM, J = decltype(q)::value * FN;
+        const int64_t m0 = m_blk + OpA::at(decltype(p)::value, (wave / S::GN) * OpA::ROWS);
+        const int64_t n0 = n_blk + OpB::at(decltype(q)::value, (wave % S::GN) * OpB::ROWS);
+        typename OP::acc_t part[FM][FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                part[i][j] = acc[I + i][J + j];
+        if (a.d_kind == OUT_F32)
+            epilogue_slabs<OP, FM, FN, OUT_F32, C>(e, part, m0, n0, lane, lds);
+        else if (a.d_kind == OUT_F16)
+            epilogue_slabs<OP, FM, FN, OUT_F16, C>(e, part, m0, n0, lane, lds);
+        else
+            epilogue_slabs<OP, FM, FN, OUT_BF16, C>(e, part, m0, n0, lane, lds);
+    };
+    auto pieces = [&](auto cpol) STG_AI {
+        store(I0{}, I0{}, cpol);
+        if constexpr (PB == 2)
+            store(I0{}, I1{}, cpol);
+        if constexpr (PA == 2)
+            store(I1{}, I0{}, cpol);
+        if constexpr (PA == 2 && PB == 2)
+            store(I1{}, I1{}, cpol);
+    };
+    // Whole cache lines go past the caches (2-8 % faster where the operands
+    // want them), parts of lines have to meet there: with rows of 60.25 lines
+    // non-temporal stores took 163 us, plain ones 67 (12 groups of 2944 x
+    // 1928).
+    if (a.whole_lines)
+        pieces(std::integral_constant<int, EPI_CPOL>{});
+    else
+        pieces(std::integral_constant<int, 0>{});
+}
+
 // One BM x BN tile of group t at (m_blk, n_blk); M, K: its group's rows (of
 // the output) and sum.
 template <class OP, bool W, int ALAY, int BLAY, int BM, int BN>
@@ -256,12 +387,10 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
                                         int64_t n_blk, int64_t M, int64_t K, int lane, int wave,
                                         const Regions &L)
 {
-    constexpr bool BF = std::is_same<OP, Op16BF16>::value;
-    constexpr int RA = BM / 2, RB = BN / 2;   // rows (columns) of a region
-    constexpr int WM = BM / 2, WN = BN / 4;   // a wave's block
-    constexpr int FA = WM / 32, FB = WN / 32; // fragments of one of its halves
-    typedef Operand<ALAY, RA, WM / 2, BF> OpA;
-    typedef Operand<BLAY, RB, WN / 2, BF> OpB;
+    typedef TileShape<OP, W, ALAY, BLAY, BM, BN> S;
+    constexpr int FA = S::FA, FB = S::FB;
+    typedef typename S::OpA OpA;
+    typedef typename S::OpB OpB;
     auto reg_a = [&](auto half, auto buf) STG_AI -> uint8_t * {
         if constexpr (decltype(buf)::value == 0)
             return decltype(half)::value == 0 ? L.a00 : L.a10;
@@ -276,37 +405,9 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
     };
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
-    const int wm = wave >> 2, wn = wave & 3;
-
     OpA A;
     OpB B;
-    A.ld = a.lda * 2;
-    if constexpr (ALAY == GL_K) {
-        A.base = (const uint8_t *)a.A + (t.r0 + m_blk) * A.ld;
-        A.k_bytes = K * 2;
-        A.span = M - m_blk;
-    } else {
-        A.base = (const uint8_t *)a.A + t.r0 * A.ld + m_blk * 2;
-        A.k_bytes = K;
-        A.span = (M - m_blk) * 2;
-    }
-    constexpr int BE = BLAY == GL_Q8 ? 1 : 2;
-    B.ld = a.ldb * BE;
-    if constexpr (BLAY == GL_K) {
-        B.base = (const uint8_t *)a.B + ((int64_t)t.g * a.N + n_blk) * B.ld;
-        B.k_bytes = K * 2;
-        B.span = a.N - n_blk;
-    } else {
-        B.base = (const uint8_t *)a.B + (W ? t.r0 : (int64_t)t.g * a.K) * B.ld + n_blk * BE;
-        B.k_bytes = K;
-        B.span = (a.N - n_blk) * BE;
-    }
-    if constexpr (BLAY == GL_Q8) {
-        B.ld_sc = (a.N + 31) / 32;
-        B.sc = a.bs + t.r0 * B.ld_sc + n_blk / 32;
-    }
-    A.init(lane, wave, wm);
-    B.init(lane, wave, wn);
+    set_operands<S>(A, B, a, t, m_blk, n_blk, M, K, lane, wave);
 
     typename OP::acc_t acc[2 * FA][2 * FB];
 #pragma unroll
@@ -332,21 +433,9 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
                 for (int r = 0; r < FB; ++r)
                     fb[decltype(half)::value][r][s] = B.read(reg_b(half, buf), r, s);
         };
-        // keeps a memory phase's steps in their order
-        auto step = [&]() STG_AI {
-            STG_COMPILER_FENCE();
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        auto barrier = [&]() STG_AI {
-            STG_COMPILER_FENCE();
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-            STG_COMPILER_FENCE();
-        };
         auto mfma = [&](auto ha, auto hb) STG_AI {
             constexpr int P = decltype(ha)::value, Q = decltype(hb)::value;
-            barrier();
+            tile_barrier();
             __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0)
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_setprio(1);
@@ -360,7 +449,7 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
                             OP::mma((const uint32_t *)&fa[i][s], (const uint32_t *)&fb[Q][j][s],
                                     acc[P * FA + i][Q * FB + j]);
             __builtin_amdgcn_s_setprio(0);
-            barrier();
+            tile_barrier();
         };
         // vector-memory instructions of the five clusters up to and with one
         // that copies A (B): what may be in flight when the copies of the
@@ -383,29 +472,29 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
             using P = decltype(pc);
             using N = std::integral_constant<int, 1 - P::value>;
             read_a(I0{}, P{});
-            step();
+            in_order();
             A.copy(reg_a(I1{}, N{}), I1{}, kt + 1, wave);
-            step();
+            in_order();
             STG_WAIT_VMCNT(AFTER_B);
             mfma(I0{}, I0{});
             read_b(I1{}, P{});
             put_b(I0{}, N{});
-            step();
+            in_order();
             B.copy(reg_b(I0{}, P{}), I0{}, kt + 2, wave);
-            step();
+            in_order();
             STG_WAIT_VMCNT(AFTER_A);
             mfma(I0{}, I1{});
             read_a(I1{}, P{});
-            step();
+            in_order();
             A.copy(reg_a(I0{}, P{}), I0{}, kt + 2, wave);
-            step();
+            in_order();
             STG_WAIT_VMCNT(AFTER_B);
             mfma(I1{}, I0{});
             read_b(I0{}, N{});
             put_b(I1{}, N{});
-            step();
+            in_order();
             B.copy(reg_b(I1{}, P{}), I1{}, kt + 2, wave);
-            step();
+            in_order();
             STG_WAIT_VMCNT(AFTER_A);
             mfma(I1{}, I1{});
         };
@@ -422,11 +511,11 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
         B.copy(reg_b(I1{}, I1{}), I1{}, 1, wave);
         STG_WAIT_VMCNT(3 * VB + 2 * VA);
         __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0): 8-bit B's stores
-        barrier();
+        tile_barrier();
         read_b(I0{}, I0{});
         __builtin_amdgcn_s_waitcnt(0xC07F); // (read before anyone copies over it)
         if (wave >= 4)
-            barrier(); // the trailing half starts one phase later
+            tile_barrier(); // the trailing half starts one phase later
         int kt = 0;
         for (; kt + 1 < KT; kt += 2) {
             tile(I0{}, kt);
@@ -435,9 +524,9 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
         if (kt < KT)
             tile(I0{}, kt);
         if (wave < 4)
-            barrier();
+            tile_barrier();
         STG_WAIT_VMCNT(0); // copies past the last tile, before LDS is reused
-        barrier();
+        tile_barrier();
     }
 
     // a wave's slab of 32 rows lies in the region of its number
@@ -449,36 +538,98 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
                     : wave == 5 ? L.b10
                     : wave == 6 ? L.b01
                                 : L.b11;
-    EpiArgs e = group_epilogue(a, t.g, t.r0, M);
-    e.vec = a.vec;
-    uint32_t *const lds = (uint32_t *)slab;
-    // the wave's block, in as many pieces as its rows and columns lie in
-    constexpr int PA = OpA::KC ? 1 : 2, PB = OpB::KC ? 1 : 2;
-    auto store = [&](auto p, auto q) STG_AI {
-        constexpr int FM = 2 * FA / PA, FN = 2 * FB / PB;
-        constexpr int I = decltype(p)::value * FM, J = decltype(q)::value * FN;
-        const int64_t m0 = m_blk + OpA::at(decltype(p)::value, wm * (WM / 2));
-        const int64_t n0 = n_blk + OpB::at(decltype(q)::value, wn * (WN / 2));
-        typename OP::acc_t part[FM][FN];
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                part[i][j] = acc[I + i][J + j];
-        if (a.d_kind == OUT_F32)
-            epilogue_slabs<OP, FM, FN, OUT_F32>(e, part, m0, n0, lane, lds);
-        else if (a.d_kind == OUT_F16)
-            epilogue_slabs<OP, FM, FN, OUT_F16>(e, part, m0, n0, lane, lds);
-        else
-            epilogue_slabs<OP, FM, FN, OUT_BF16>(e, part, m0, n0, lane, lds);
+    store_tile<OP, S>(a, t, m_blk, n_blk, M, acc, lane, wave, (uint32_t *)slab);
+}
+
+// A 64 x 64 tile, for products of few tiles: there the time is a workgroup's
+// way through K at the rate one compute unit's copies reach (measured about
+// 60 GB/s), and four times the workgroups each copy half as much.  Four
+// waves, four buffers s[0..3], the copies of three K tiles in flight, one
+// barrier per K tile: before it every wave has waited for its copies of tile
+// t and has tile t - 1 in registers (lgkmcnt(0) before its MFMAs); after it
+// the copies of t + 3 go where t - 1 was.  An 8-bit B of tile t + 1 (loaded two
+// tiles before) is stored after the reads of t.
+template <class OP, bool W, int ALAY, int BLAY>
+__device__ STG_AI inline void small_body(const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
+                                         int64_t n_blk, int64_t M, int64_t K, int lane, int wave,
+                                         uint8_t *s0, uint8_t *s1, uint8_t *s2, uint8_t *s3)
+{
+    typedef SmallShape<OP, W, ALAY, BLAY> S;
+    constexpr int RB = 64 * 128; // bytes of a region: A, B in a buffer
+    typename S::OpA A;
+    typename S::OpB B;
+    set_operands<S>(A, B, a, t, m_blk, n_blk, M, K, lane, wave);
+    typename OP::acc_t acc[2][2] = {};
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+    auto buf = [&](auto b) STG_AI {
+        constexpr int P = decltype(b)::value;
+        return P == 0 ? s0 : P == 1 ? s1 : P == 2 ? s2 : s3;
     };
-    store(I0{}, I0{});
-    if constexpr (PB == 2)
-        store(I0{}, I1{});
-    if constexpr (PA == 2)
-        store(I1{}, I0{});
-    if constexpr (PA == 2 && PB == 2)
-        store(I1{}, I1{});
+    // K tile kt: buffer and register set by its last bits, b
+    auto copy = [&](auto b, int kt) STG_AI {
+        A.copy(buf(b), I0{}, kt, wave);
+        B.template copy<decltype(b)::value & 1>(buf(b) + RB, I0{}, kt, wave);
+    };
+    auto put_b = [&](auto b) STG_AI {
+        if constexpr (BLAY == GL_Q8)
+            B.template store<decltype(b)::value & 1>(buf(b) + RB, I0{}, lane, wave);
+    };
+    constexpr int PER = S::OpA::VM + S::OpB::VM; // vector-memory instructions of copy()
+    const int KT = (int)((K + 63) / 64);
+    auto tile = [&](auto b, int kt) STG_AI {
+        constexpr int P = decltype(b)::value;
+        in_order();
+        STG_WAIT_VMCNT(2 * PER);
+        tile_barrier();
+        u4_t fa[2][2], fb[2][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                fa[r][s] = A.read(buf(b), r, s);
+                fb[r][s] = B.read(buf(b) + RB, r, s);
+            }
+        put_b(std::integral_constant<int, (P + 1) & 3>{});
+        in_order();
+        copy(std::integral_constant<int, (P + 3) & 3>{}, kt + 3);
+        in_order();
+        __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = OP::mma((const uint32_t *)&fa[i][s], (const uint32_t *)&fb[j][s],
+                                        acc[i][j]);
+    };
+    if (KT > 0) {
+        copy(I0{}, 0);
+        copy(I1{}, 1);
+        put_b(I0{});
+        copy(I2{}, 2);
+        __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0): 8-bit B's stores
+        int kt = 0;
+        for (; kt + 3 < KT; kt += 4) {
+            tile(I0{}, kt);
+            tile(I1{}, kt + 1);
+            tile(I2{}, kt + 2);
+            tile(I3{}, kt + 3);
+        }
+        if (kt < KT)
+            tile(I0{}, kt);
+        if (kt + 1 < KT)
+            tile(I1{}, kt + 1);
+        if (kt + 2 < KT)
+            tile(I2{}, kt + 2);
+        STG_WAIT_VMCNT(0); // copies past the last tile, before LDS is reused
+        tile_barrier();
+    }
+    uint8_t *slab = wave == 0 ? s0 : wave == 1 ? s1 : wave == 2 ? s2 : s3;
+    store_tile<OP, S>(a, t, m_blk, n_blk, M, acc, lane, wave, (uint32_t *)slab);
 }
 
 // The kernel.  The rows' product with 256-row tiles (SHORT) cuts a group's
@@ -563,6 +714,42 @@ __global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_grouped_t
         }
         tile_body<OP, W, ALAY, BLAY, BM, BN>(a, t, m, n, M, a.K, lane, wave, L);
     }
+}
+
+// The kernel of 64 x 64 tiles, two workgroups per compute unit.
+template <class OP, bool W, int ALAY, int BLAY>
+__global__ __launch_bounds__(256, 2) void k_grouped_small(GroupedArgs a, int tiles_m, int tiles_n)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[16384], s1[16384], s2[16384], s3[16384];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    GroupRows t;
+    int tm, tn;
+    if constexpr (W) {
+        const int per = (tiles_m * tiles_n + 7) >> 3, slot = blockIdx.x >> 3;
+        const int tile = (blockIdx.x & 7) * per + slot % per;
+        if (tile >= tiles_m * tiles_n)
+            return;
+        int b, e;
+        t.g = slot / per;
+        tile_of(tile, tiles_m, tiles_n, tm, tn);
+        group_bounds(a, t.g, b, e);
+        t.r0 = __builtin_amdgcn_readfirstlane(b);
+        t.r1 = __builtin_amdgcn_readfirstlane(e);
+    } else {
+        int n_long, n_short;
+        count_tiles<64, false>(a, lane, n_long, n_short);
+        const int id = xcd_tile(blockIdx.x, n_long * tiles_n);
+        if (id < 0)
+            return;
+        tile_of(id, n_long, tiles_n, tm, tn);
+        if (!find_tile<64, false>(a, __builtin_amdgcn_readfirstlane(tm), n_long, lane, t))
+            return;
+        tm = t.tm;
+    }
+    const int64_t M = W ? a.K : t.r1 - t.r0, K = W ? t.r1 - t.r0 : a.K;
+    small_body<OP, W, ALAY, BLAY>(a, t, wave_uniform((int64_t)tm * 64), wave_uniform((int64_t)tn * 64),
+                                 M, K, lane, wave, s0, s1, s2, s3);
 }
 
 } // namespace stg

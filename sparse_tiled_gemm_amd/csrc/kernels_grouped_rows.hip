@@ -17,11 +17,22 @@ static hipError_t launch_t(const GroupedArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
+template <class OP, int BLAY>
+static hipError_t launch_small(const GroupedArgs &a, hipStream_t s)
+{
+    const int tiles_n = (int)((a.N + 63) / 64);
+    const dim3 grid((unsigned)((max_row_tiles<64>(a) * tiles_n + 7) / 8 * 8));
+    hipLaunchKernelGGL((k_grouped_small<OP, false, GL_K, BLAY>), grid, dim3(256), 0, s, a, 0, tiles_n);
+    return hipGetLastError();
+}
+
 template <class OP>
 static hipError_t launch_op(int family, const GroupedArgs &a, hipStream_t s)
 {
     if (family == GF_TILED_256)
         return a.b_row ? launch_t<OP, GL_MN, 256, 256>(a, s) : launch_t<OP, GL_K, 256, 256>(a, s);
+    if (family == GF_TILED_64)
+        return a.b_row ? launch_small<OP, GL_MN>(a, s) : launch_small<OP, GL_K>(a, s);
     return a.b_row ? launch_t<OP, GL_MN, 128, 128>(a, s) : launch_t<OP, GL_K, 128, 128>(a, s);
 }
 

@@ -16,11 +16,24 @@ static hipError_t launch_t(const GroupedArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
+template <class OP, int BLAY>
+static hipError_t launch_small(const GroupedArgs &a, hipStream_t s)
+{
+    const int tiles_m = (int)((a.K + 63) / 64), tiles_n = (int)((a.N + 63) / 64);
+    const int64_t per_xcd = ((int64_t)tiles_m * tiles_n + 7) / 8;
+    const dim3 grid((unsigned)(per_xcd * 8 * a.groups));
+    hipLaunchKernelGGL((k_grouped_small<OP, true, GL_MN, BLAY>), grid, dim3(256), 0, s, a, tiles_m,
+                       tiles_n);
+    return hipGetLastError();
+}
+
 template <class OP>
 static hipError_t launch_op(int family, const GroupedArgs &a, hipStream_t s)
 {
     if (family == GF_TILED_256)
         return a.bs ? launch_t<OP, GL_Q8, 256, 256>(a, s) : launch_t<OP, GL_MN, 256, 256>(a, s);
+    if (family == GF_TILED_64)
+        return a.bs ? launch_small<OP, GL_Q8>(a, s) : launch_small<OP, GL_MN>(a, s);
     return a.bs ? launch_t<OP, GL_Q8, 128, 128>(a, s) : launch_t<OP, GL_MN, 128, 128>(a, s);
 }
 

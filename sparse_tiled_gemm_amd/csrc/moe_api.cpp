@@ -370,9 +370,63 @@ static bool grouped_tiled_ok(const gemm_grouped_desc_t &d)
            d.lda < lim && d.ldb < lim;
 }
 
+// The family for a descriptor the tiled kernels take, from its sizes alone
+// (the plan cannot see the groups' bounds; every family serves groups of any
+// length).  Times are us on MI355X.
+static int choose_family(const gemm_grouped_desc_t &d, int num_cu)
+{
+    auto tiles = [](int64_t n, int64_t b) { return ceil_div(n, b); };
+    if (d.mode == GEMM_GROUPED_WEIGHTS) {
+        // While 64 x 64 tiles fit the chip at once (two per compute unit) a
+        // tile's way through the rows is the time: 4 groups of 3400 rows, 704
+        // x 480, 34 with 64, 68 with 128; 2048 x 1024, 65 and 59.  The same
+        // for 128 against 256: 4 groups of 2048 rows, 2048 x 1024, 57 and 75;
+        // 2048 x 4096, 199 and 144.
+        const int64_t t64 = d.groups * tiles(d.K, 64) * tiles(d.N, 64);
+        const int64_t t128 = d.groups * tiles(d.K, 128) * tiles(d.N, 128);
+        const int64_t t256 = d.groups * tiles(d.K, 256) * tiles(d.N, 256);
+        if (t64 <= 2 * num_cu)
+            return GF_TILED_64;
+        if (t128 <= 2 * num_cu)
+            return GF_TILED_128;
+        // Many tiles: 256 moves less per product, 128 wastes less at the
+        // edges and, two to a compute unit, hides its stores better, which
+        // counts where the groups are short: 40 groups of 365 rows, 2136 x
+        // 384, 116 and 92; 17 groups of 36 rows, 488 x 3720, 50 and 47 (16 of
+        // 62 rows, 4096 x 2048, whole cache lines: 196 and 254); 3 groups of
+        // 1400, 6400 x 1240, 110 and 137.
+        if (d.rows >= 512 * (int64_t)d.groups)
+            return t256 * 4 * 3 <= t128 * 4 ? GF_TILED_256 : GF_TILED_128;
+        const bool lines = d.ldd * (d.d_type == GEMM_F32 ? 4 : 2) % 128 == 0;
+        return lines && t256 * 4 * 10 <= t128 * 11 ? GF_TILED_256 : GF_TILED_128;
+    }
+    // Rows: groups that can have rows, and the row tiles expected of them
+    // (each wastes half a tile).
+    const int64_t g = d.groups < d.rows ? d.groups : d.rows;
+    auto expect = [&](int64_t b) { return (d.rows / b + (g + 1) / 2) * tiles(d.N, b); };
+    // Few tiles: time is one workgroup's way through K.  Up to 16 rows per
+    // group the skinny kernel, whose waves split K (4 groups, 1024 x 2048: 4
+    // rows 6.0 against 9.6, 16 rows 7.2 and 9.7, 64 rows 9.7 and 9.8), then 64
+    // x 64 tiles (367 rows, 352 x 4880, 24 against 45 with 128; 6 groups of
+    // 324, 1072 x 1616, 26 and 25).
+    if (expect(64) <= 2 * num_cu)
+        return d.rows <= 16 * g ? GF_SKINNY : GF_TILED_64;
+    // Few rows per group: bound by B's stream.  32 groups, 4096 x 2048, with
+    // 64 / 128 / 256: 4 rows each 109 / 123 / 122, 16 rows 114 / 125 / 132, 32
+    // rows 131 / 132 / 135; row-major B, read in runs of a tile's width: 2
+    // rows 84 / 89 / 88, 4 rows 110 / 109 / 99, 16 rows 131 / 138 / 108.
+    if (d.rows < 32 * g)
+        return d.b_layout == GEMM_ROW_MAJOR && d.rows >= 4 * g ? GF_TILED_256 : GF_TILED_64;
+    // 8 groups of 256 rows, 2048 x 1024, 19 with 128 and 20 with 256, x 4096
+    // 77 and 67; 15 groups of 208, 1504 x 408, 15 and 17; 8 of 1024, 2048 x
+    // 1024, 52 and 47.
+    return expect(128) <= (d.K <= 1024 ? 2 : 1) * (int64_t)num_cu ? GF_TILED_128 : GF_TILED_256;
+}
+
 static const char *grouped_family_name(int f)
 {
-    static const char *const n[GF_COUNT] = {"generic", "skinny", "tiled128", "tiled256"};
+    static const char *const n[GF_COUNT] = {"generic", "skinny", "tiled64", "tiled128",
+                                             "tiled256"};
     return n[f];
 }
 
@@ -388,35 +442,12 @@ gemm_status_t gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_pl
     DeviceInfo di;
     CHECK(check_device(&dev, &di));
     const bool tiled = grouped_tiled_ok(d);
-    // 256- against 128-wide tiles, us on MI355X.  Rows: once the expected
-    // 128-wide tiles (half a tile per group wasted) no longer fit one per
-    // compute unit, and from about 32 rows per group (8 groups, K 1024: 512 x
-    // 2048 17 and 13, 2048 x 2048 20 and 19, 8192 x 2048 47 and 52; 32 groups
-    // of 16 rows, 4096 x 2048 140 and 125).  Weights: once the 128-wide ones,
-    // two per compute unit, no longer fit at once (4 groups of 2048 rows, 2048
-    // x 1024 75 and 57, 2048 x 4096 144 and 199; 32 groups of 256 rows, 512 x
-    // 256 35 and 20, 512 x 4096 82 and 98).
-    const int64_t tiles_n = ceil_div(d.N, 128);
-    const bool small = d.mode == GEMM_GROUPED_WEIGHTS
-                           ? d.groups * ceil_div(d.K, 128) * tiles_n <= 2 * di.num_cu
-                           : d.rows < 32 * (int64_t)d.groups ||
-                                 (d.rows / 128 + d.groups / 2) * tiles_n <= di.num_cu;
-    const int auto_tiled = small ? GF_TILED_128 : GF_TILED_256;
-    // Few rows per group: B's stream bounds the product (the plan cannot see
-    // the groups' bounds; every family serves groups of any length).  With B
-    // 32 x 4096 x 2048 the skinny kernel and the 128 x 128 tile took 109 and
-    // 123 us at 4 rows per group, 138 and 125 us at 16 (row-major B: 126 and
-    // 137 us at 16, 145 and 145 us at 32); where the 128-wide tiles leave
-    // compute units idle its split along K helps longer: 4 groups of 1024 x
-    // 2048, 8 and 20 us at 4 rows each, 10 and 20 at 16, 20 and 20 at 64.
-    const bool skinny = tiled && d.mode == GEMM_GROUPED_ROWS;
-    const int64_t wide = (ceil_div(d.rows, 128) + (d.groups < d.rows ? d.groups : d.rows)) *
-                         ceil_div(d.N, 128);
-    const int64_t few_rows = wide < di.num_cu ? 48 : d.b_layout == GEMM_ROW_MAJOR ? 24 : 10;
-    const bool few = d.rows <= few_rows * d.groups;
+    const bool skinny = tiled && d.mode == GEMM_GROUPED_ROWS; // (can serve)
+    const int auto_fam = tiled ? choose_family(d, di.num_cu) : GF_GENERIC;
+    const int auto_tiled = auto_fam == GF_SKINNY ? GF_TILED_64 : auto_fam;
     int fam = -1;
     switch (d.algo) {
-    case GEMM_ALGO_AUTO: fam = skinny && few ? GF_SKINNY : tiled ? auto_tiled : GF_GENERIC; break;
+    case GEMM_ALGO_AUTO: fam = auto_fam; break;
     case GEMM_ALGO_SKINNY: fam = skinny ? GF_SKINNY : -1; break;
     case GEMM_ALGO_GENERIC: fam = GF_GENERIC; break;
     case GEMM_ALGO_TILED: fam = tiled ? auto_tiled : -1; break;
@@ -424,6 +455,13 @@ gemm_status_t gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_pl
     case GEMM_ALGO_TILED_256: fam = tiled ? GF_TILED_256 : -1; break;
     default: fam = -1;
     }
+    // Tuning override, as in gemm_plan: STGEMM_FORCE_KERNEL=<family name>
+    // replaces the choice for descriptors that family can serve.
+    if (const char *force = getenv("STGEMM_FORCE_KERNEL"))
+        for (int f = 0; f < GF_COUNT; ++f)
+            if (strcmp(force, grouped_family_name(f)) == 0 &&
+                (f == GF_GENERIC || (f == GF_SKINNY ? skinny : tiled)))
+                fam = f;
     if (fam < 0)
         return fail(GEMM_ERR_UNSUPPORTED, "requested algorithm cannot serve this problem");
     gemm_grouped_plan_t *p = new (std::nothrow) gemm_grouped_plan_t();
@@ -507,6 +545,7 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_plan_t *plan, const void *A, c
     a.num_cu = plan->num_cu;
     a.vec = (!d.has_c || aligned(C, 4 * (size_t)db)) && aligned(D, 4 * (size_t)db) &&
             d.ldd % 4 == 0 && d.ldd * db < 0x7fffffff / 257;
+    a.whole_lines = aligned(D, 128) && (d.ldd * db) % 128 == 0;
     int fam = plan->family;
     if (fam != GF_GENERIC && (!aligned(A, 16) || !aligned(B, 16)))
         fam = GF_GENERIC;

@@ -71,6 +71,7 @@ hipError_t launch_swiglu_backward(const Q8Args &a, hipStream_t s);
 enum GroupedFamily {
     GF_GENERIC = 0,
     GF_SKINNY,    // rows: few per group
+    GF_TILED_64,  // 64 x 64 tiles: few tiles
     GF_TILED_128, // 128 x 128 tiles, two workgroups per compute unit
     GF_TILED_256, // 256 x 256 tiles, one
     GF_COUNT
@@ -91,6 +92,7 @@ struct GroupedArgs {
     int d_kind; // OutKind
     int num_cu; // compute units of the device
     int vec;    // rows of C and D allow the vector epilogue (EpiArgs::vec)
+    int whole_lines; // D's rows start on cache lines
 };
 // one-launch grid limits and operand requirements are checked by the plan
 hipError_t launch_grouped_rows(int family, const GroupedArgs &a, hipStream_t s);    // tiled

@@ -1,5 +1,7 @@
 """Grouped products (gemm_grouped_run) on the GPU against plain 64-bit
 products, group by group, for every kernel family that takes the sizes."""
+import os
+
 import pytest
 import torch
 
@@ -9,17 +11,21 @@ from sparse_tiled_gemm_amd import gemm as G
 
 pytestmark = pytest.mark.gpu
 
-FAMILIES = ["auto", "generic", "skinny", "tiled128", "tiled256"]
+FAMILIES = ["auto", "generic", "skinny", "tiled64", "tiled128", "tiled256"]
 
 
 def _plan(algo, *a, **kw):
-    """A plan, or a skip where the forced family does not take the sizes."""
+    """A plan of the family (through the tuning override), or a skip where it
+    does not take the sizes."""
+    if algo != "auto":
+        os.environ["STGEMM_FORCE_KERNEL"] = algo
     try:
-        return G.gemm_grouped_plan(G.make_grouped_desc(*a, algo=algo, **kw))
-    except G.GemmError as e:
-        if algo != "auto" and e.status == G.GEMM_ERR_UNSUPPORTED:
-            pytest.skip("%s does not take these sizes" % algo)
-        raise
+        plan = G.gemm_grouped_plan(G.make_grouped_desc(*a, **kw))
+    finally:
+        os.environ.pop("STGEMM_FORCE_KERNEL", None)
+    if algo != "auto" and "_%s_" % algo not in plan.name:
+        pytest.skip("%s does not take these sizes" % algo)
+    return plan
 
 
 def _mat(gen, rows, cols, dtype, ld=0, scale=1.0, off=0):
@@ -252,3 +258,17 @@ def test_weights_of_other_groups_do_not_leak(algo, eight):
     torch.cuda.synchronize()
     d = D.cpu()
     assert torch.isfinite(d[0]).all() and torch.isfinite(d[2]).all() and torch.isnan(d[1]).all()
+
+
+@pytest.mark.parametrize("algo", ["skinny", "tiled128", "tiled256"])
+def test_forced_algorithms(algo):
+    """The descriptor's algo code picks the family too, or is refused."""
+    d = lambda mode, K=64: G.make_grouped_desc(mode, 64, 64, K, 4, "bf16", "bf16", "bf16", algo=algo)
+    assert algo in G.gemm_grouped_plan(d("rows")).name
+    with pytest.raises(G.GemmError):
+        G.gemm_grouped_plan(d("rows", 65))  # rows of A not in whole 16 bytes
+    if algo == "skinny":
+        with pytest.raises(G.GemmError):
+            G.gemm_grouped_plan(d("weights"))
+    else:
+        assert algo in G.gemm_grouped_plan(d("weights")).name
