@@ -329,43 +329,42 @@ __global__ __launch_bounds__(256) void k_combine(RowsArgs r)
 }
 
 // The gradient of k_combine: per token, each choice's row of dYs and the dot
-// product of its row of Ys with dY.  TPT lanes per token (a wave, or a
-// workgroup of four where there are few tokens); KB choices share one pass
-// over dY.
-constexpr int CB_K = 4;
-template <bool BF, int TPT>
+// product of its row of Ys with dY.  TPT lanes per token: a part of a wave for
+// narrow rows, a wave, or a workgroup of four where there are few tokens; KB
+// choices share one pass over dY.
+template <bool BF, int TPT, int KB>
 __global__ __launch_bounds__(256) void k_combine_backward(RowsArgs r)
 {
-    __shared__ float part[256 / 64][CB_K];
+    __shared__ float part[256 / 64][KB];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     // (t is uniform over the lanes of a token, and over the workgroup where
     // it meets at barriers)
     int64_t t = (int64_t)blockIdx.x * (256 / TPT) + threadIdx.x / TPT;
     for (; t < r.tokens; t += (int64_t)gridDim.x * (256 / TPT)) {
-    const uint16_t *dy = (const uint16_t *)r.in + t * r.ld_in;
-    for (int64_t k0 = 0; k0 < r.topk; k0 += CB_K) {
-        float acc[CB_K] = {}, w[CB_K];
-        int64_t p[CB_K];
+        const uint16_t *dy = (const uint16_t *)r.in + t * r.ld_in;
+        for (int64_t k0 = 0; k0 < r.topk; k0 += KB) {
+            float acc[KB] = {}, w[KB];
+            int64_t p[KB];
 #pragma unroll
-        for (int q = 0; q < CB_K; ++q) {
-            const int64_t s = t * r.topk + k0 + q;
-            const bool in = k0 + q < r.topk;
-            p[q] = in ? r.pos[s] : -1;
-            p[q] = p[q] < r.rows ? p[q] : -1;
-            w[q] = in ? r.weights[s] : 0.0f;
-        }
+            for (int q = 0; q < KB; ++q) {
+                const int64_t s = t * r.topk + k0 + q;
+                const bool in = k0 + q < r.topk;
+                p[q] = in ? r.pos[s] : -1;
+                p[q] = p[q] < r.rows ? p[q] : -1;
+                w[q] = in ? r.weights[s] : 0.0f;
+            }
             for (int64_t c = (threadIdx.x % TPT) * 8; c < r.cols; c += TPT * 8) {
                 const int n = (int)min((int64_t)8, r.cols - c);
-                u4_t y[CB_K];
+                u4_t y[KB];
                 float d[8];
                 const u4_t dv = load8(dy + c, n);
 #pragma unroll
-                for (int q = 0; q < CB_K; ++q)
+                for (int q = 0; q < KB; ++q)
                     if (p[q] >= 0)
                         y[q] = load8((const uint16_t *)r.in2 + p[q] * r.ld_in2 + c, n);
                 widen8<BF>(dv, d);
 #pragma unroll
-                for (int q = 0; q < CB_K; ++q)
+                for (int q = 0; q < KB; ++q)
                     if (p[q] >= 0) {
                         float f[8], g[8];
                         widen8<BF>(y[q], f);
@@ -378,33 +377,33 @@ __global__ __launch_bounds__(256) void k_combine_backward(RowsArgs r)
                     }
             }
 #pragma unroll
-        for (int q = 0; q < CB_K; ++q) {
+            for (int q = 0; q < KB; ++q) {
 #pragma unroll
-            for (int d = 32; d; d >>= 1)
-                acc[q] += __shfl_xor(acc[q], d);
-        }
-        if constexpr (TPT == 64) {
-            if (lane == 0)
-#pragma unroll
-                for (int q = 0; q < CB_K; ++q)
-                    if (k0 + q < r.topk)
-                        r.dw[t * r.topk + k0 + q] = acc[q];
-        } else {
-            if (lane == 0)
-#pragma unroll
-                for (int q = 0; q < CB_K; ++q)
-                    part[wave][q] = acc[q];
-            __syncthreads();
-            if (threadIdx.x < CB_K && k0 + threadIdx.x < r.topk) {
-                float x = 0.0f;
-#pragma unroll
-                for (int w2 = 0; w2 < 256 / 64; ++w2)
-                    x += part[w2][threadIdx.x];
-                r.dw[t * r.topk + k0 + threadIdx.x] = x;
+                for (int d = (TPT < 64 ? TPT : 64) / 2; d; d >>= 1)
+                    acc[q] += __shfl_xor(acc[q], d);
             }
-            __syncthreads();
+            if constexpr (TPT <= 64) {
+                if (lane % TPT == 0)
+#pragma unroll
+                    for (int q = 0; q < KB; ++q)
+                        if (k0 + q < r.topk)
+                            r.dw[t * r.topk + k0 + q] = acc[q];
+            } else {
+                if (lane == 0)
+#pragma unroll
+                    for (int q = 0; q < KB; ++q)
+                        part[wave][q] = acc[q];
+                __syncthreads();
+                if (threadIdx.x < KB && k0 + threadIdx.x < r.topk) {
+                    float x = 0.0f;
+#pragma unroll
+                    for (int w2 = 0; w2 < 256 / 64; ++w2)
+                        x += part[w2][threadIdx.x];
+                    r.dw[t * r.topk + k0 + threadIdx.x] = x;
+                }
+                __syncthreads();
+            }
         }
-    }
     }
 }
 
@@ -486,20 +485,30 @@ hipError_t launch_combine(const RowsArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
-template <bool BF>
+template <bool BF, int TPT>
 static void combine_backward_t(const RowsArgs &a, hipStream_t s)
 {
-    if (a.tokens < 2048)
-        hipLaunchKernelGGL((k_combine_backward<BF, 256>), dim3(blocks(a.tokens, 1)), dim3(256), 0, s,
-                           a);
+    const dim3 grid(blocks(a.tokens, 256 / TPT));
+    if (a.topk <= 4)
+        hipLaunchKernelGGL((k_combine_backward<BF, TPT, 4>), grid, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((k_combine_backward<BF, 64>), dim3(blocks(a.tokens, 4)), dim3(256), 0, s,
-                           a);
+        hipLaunchKernelGGL((k_combine_backward<BF, TPT, 8>), grid, dim3(256), 0, s, a);
+}
+
+template <bool BF>
+static void combine_backward_lanes(const RowsArgs &a, hipStream_t s)
+{
+    if (a.cols <= 256)
+        combine_backward_t<BF, 16>(a, s);
+    else if (a.tokens >= 2048)
+        combine_backward_t<BF, 64>(a, s);
+    else
+        combine_backward_t<BF, 256>(a, s);
 }
 
 hipError_t launch_combine_backward(const RowsArgs &a, hipStream_t s)
 {
-    a.bf16 ? combine_backward_t<true>(a, s) : combine_backward_t<false>(a, s);
+    a.bf16 ? combine_backward_lanes<true>(a, s) : combine_backward_lanes<false>(a, s);
     return hipGetLastError();
 }
 

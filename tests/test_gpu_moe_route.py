@@ -71,6 +71,7 @@ CASES = [  # tokens, topk, groups, cols, dtype, drop, ld extra, element offset
     (129, 3, 5, 1027, "f16", 0.1, 0, 0), (700, 5, 9, 515, "bf16", 0.3, 3, 1),
     (2100, 1, 16, 72, "bf16", 0.0, 0, 0), (2049, 6, 30, 24, "f16", 0.5, 0, 3),
     (2800, 3, 20, 520, "f16", 0.1, 0, 0), (4200, 2, 11, 40, "bf16", 0.0, 0, 0),
+    (500, 6, 21, 157, "f16", 0.05, 0, 0), (33, 2, 3, 256, "bf16", 0.0, 1, 1),
     (300, 9, 12, 2056, "bf16", 0.1, 0, 0), (50, 4, 6, 64, "f16", 1.0, 0, 0),
 ]
 
