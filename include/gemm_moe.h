@@ -103,7 +103,8 @@ gemm_status_t gemm_moe_combine_backward(int64_t tokens, int64_t topk, int64_t co
  * `offsets` (groups + 1 int32, device) cuts `rows` rows into groups: group g
  * holds rows offsets[g] .. offsets[g+1] - 1.  Bounds are clamped to 0 ..
  * rows, and a group whose end is before its start is empty.  Groups must not
- * share rows in ROWS mode (ascending bounds never do).
+ * share rows in ROWS mode (ascending bounds never do; rows of several groups
+ * get an unspecified one's product, or none).
  *
  * GEMM_GROUPED_ROWS:    D[r] = cast(A[r] * B_g) for the rows r of each group:
  *     A rows x K, D rows x N row-major; B holds `groups` matrices one after
@@ -119,6 +120,10 @@ gemm_status_t gemm_moe_combine_backward(int64_t tokens, int64_t topk, int64_t co
  *     scales, and each value enters as the one gemm_q8_load of a_type gives.
  *     b_layout is ROW_MAJOR (rows contiguous along N).
  *
+ * The fast kernels move 16-byte chunks: K, lda and ldb (and N where B is
+ * row-major) in multiples of 8, leading dimensions below 2^21, A and B 16-byte
+ * aligned; everything else runs a generic kernel.
+ *
  * a_type GEMM_F16 or GEMM_BF16; d_type GEMM_F32, GEMM_F16 or GEMM_BF16; fp32
  * accumulation, one rounding.  1 <= groups <= 65535; rows, N, K below 2^31;
  * matrices of at most 2^40 elements. */
@@ -131,8 +136,9 @@ typedef struct {
     int32_t a_type, b_type, d_type; /* gemm_dtype_t */
     int32_t b_layout;               /* gemm_layout_t */
     int32_t has_c;                  /* WEIGHTS: add C */
-    int32_t algo;                   /* gemm_algo_t: AUTO, or GENERIC, SKINNY, TILED_128,
-                                       TILED_256 to force a family */
+    int32_t algo;                   /* gemm_algo_t: AUTO, or GENERIC, SKINNY (ROWS only),
+                                       TILED, TILED_128, TILED_256 to force a family
+                                       (GEMM_ERR_UNSUPPORTED if it cannot serve) */
     int64_t lda, ldb, ldd;          /* 0 = packed */
 } gemm_grouped_desc_t;
 

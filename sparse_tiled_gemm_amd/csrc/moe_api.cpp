@@ -347,12 +347,12 @@ gemm_status_t gemm_grouped_validate_desc(const gemm_grouped_desc_t *desc)
         return fail(GEMM_ERR_UNSUPPORTED, "C applies to the weights' product only");
     if (w && d.b_layout != GEMM_ROW_MAJOR)
         return fail(GEMM_ERR_UNSUPPORTED, "the weights' product takes a row-major B");
-    // one launch holds 2^32 - 1 threads: at most 2^24 - 1 workgroups of the
-    // 64 x 64 tiles of the generic kernel
+    // one launch holds 2^32 - 1 threads: below 2^23 64 x 64 tiles every kernel's
+    // grid fits (the skinny one's narrower strips are checked by the plan)
     const int64_t tiles = w ? smul(smul(ceil_div(d.K, 64), ceil_div(d.N, 64)), d.groups)
                             : smul(ceil_div(d.rows, 64) + (d.groups < d.rows ? d.groups : d.rows),
                                    ceil_div(d.N, 64));
-    if (tiles >= (1 << 24))
+    if (tiles >= (1 << 23))
         return fail(GEMM_ERR_UNSUPPORTED, "more output tiles than one launch holds");
     return ok();
 }
@@ -375,16 +375,15 @@ static bool grouped_tiled_ok(const gemm_grouped_desc_t &d)
 // length).  Times are us on MI355X.
 static int choose_family(const gemm_grouped_desc_t &d, int num_cu)
 {
-    auto tiles = [](int64_t n, int64_t b) { return ceil_div(n, b); };
     if (d.mode == GEMM_GROUPED_WEIGHTS) {
         // While 64 x 64 tiles fit the chip at once (two per compute unit) a
         // tile's way through the rows is the time: 4 groups of 3400 rows, 704
         // x 480, 34 with 64, 68 with 128; 2048 x 1024, 65 and 59.  The same
         // for 128 against 256: 4 groups of 2048 rows, 2048 x 1024, 57 and 75;
         // 2048 x 4096, 199 and 144.
-        const int64_t t64 = d.groups * tiles(d.K, 64) * tiles(d.N, 64);
-        const int64_t t128 = d.groups * tiles(d.K, 128) * tiles(d.N, 128);
-        const int64_t t256 = d.groups * tiles(d.K, 256) * tiles(d.N, 256);
+        const int64_t t64 = d.groups * ceil_div(d.K, 64) * ceil_div(d.N, 64);
+        const int64_t t128 = d.groups * ceil_div(d.K, 128) * ceil_div(d.N, 128);
+        const int64_t t256 = d.groups * ceil_div(d.K, 256) * ceil_div(d.N, 256);
         if (t64 <= 2 * num_cu)
             return GF_TILED_64;
         if (t128 <= 2 * num_cu)
@@ -396,14 +395,14 @@ static int choose_family(const gemm_grouped_desc_t &d, int num_cu)
         // 62 rows, 4096 x 2048, whole cache lines: 196 and 254); 3 groups of
         // 1400, 6400 x 1240, 110 and 137.
         if (d.rows >= 512 * (int64_t)d.groups)
-            return t256 * 4 * 3 <= t128 * 4 ? GF_TILED_256 : GF_TILED_128;
+            return t256 * 3 <= t128 ? GF_TILED_256 : GF_TILED_128; // 4/3 of the area
         const bool lines = d.ldd * (d.d_type == GEMM_F32 ? 4 : 2) % 128 == 0;
-        return lines && t256 * 4 * 10 <= t128 * 11 ? GF_TILED_256 : GF_TILED_128;
+        return lines && t256 * 40 <= t128 * 11 ? GF_TILED_256 : GF_TILED_128;
     }
     // Rows: groups that can have rows, and the row tiles expected of them
     // (each wastes half a tile).
     const int64_t g = d.groups < d.rows ? d.groups : d.rows;
-    auto expect = [&](int64_t b) { return (d.rows / b + (g + 1) / 2) * tiles(d.N, b); };
+    auto expect = [&](int64_t b) { return (d.rows / b + (g + 1) / 2) * ceil_div(d.N, b); };
     // Few tiles: time is one workgroup's way through K.  Up to 16 rows per
     // group the skinny kernel, whose waves split K (4 groups, 1024 x 2048: 4
     // rows 6.0 against 9.6, 16 rows 7.2 and 9.7, 64 rows 9.7 and 9.8), then 64
@@ -442,7 +441,11 @@ gemm_status_t gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_pl
     DeviceInfo di;
     CHECK(check_device(&dev, &di));
     const bool tiled = grouped_tiled_ok(d);
-    const bool skinny = tiled && d.mode == GEMM_GROUPED_ROWS; // (can serve)
+    // (can serve; strips of 32 columns, 512 threads each)
+    const bool skinny =
+        tiled && d.mode == GEMM_GROUPED_ROWS &&
+        smul(ceil_div(d.rows, 64) + (d.groups < d.rows ? d.groups : d.rows), ceil_div(d.N, 32)) <
+            (1 << 22);
     const int auto_fam = tiled ? choose_family(d, di.num_cu) : GF_GENERIC;
     const int auto_tiled = auto_fam == GF_SKINNY ? GF_TILED_64 : auto_fam;
     int fam = -1;
@@ -475,6 +478,13 @@ gemm_status_t gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_pl
              d.mode == GEMM_GROUPED_WEIGHTS ? "weights" : "rows", grouped_family_name(fam),
              d.a_type == GEMM_BF16 ? "bf16" : "f16", d.b_type == GEMM_F8_E4M3 ? "xe4m3" : "",
              d.mode == GEMM_GROUPED_ROWS && d.b_layout == GEMM_ROW_MAJOR ? "_brow" : "");
+    static const bool log = [] {
+        const char *v = getenv("GEMM_LOG");
+        return v && *v && strcmp(v, "0") != 0;
+    }();
+    if (log)
+        fprintf(stderr, "[stgemm] grouped plan rows=%lld N=%lld K=%lld groups=%d -> %s\n",
+                (long long)d.rows, (long long)d.N, (long long)d.K, d.groups, p->name);
     *out = p;
     return ok();
 }

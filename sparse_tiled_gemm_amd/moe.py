@@ -62,6 +62,9 @@ class ExpertMLP:
         T, K, n, h, f, t = self.tokens, self.topk, len(self.pos), self.hidden, self.inner, self.dtype
         if X.shape != (T, h) or ids.shape != (T, K) or weights.shape != (T, K):
             raise ValueError("X is tokens x H, ids and weights tokens x topk")
+        if X.dtype != self.W1.dtype or X.stride(1) != 1 or weights.dtype != torch.float32 or \
+                not (ids.is_contiguous() and weights.is_contiguous()):
+            raise ValueError("X in the weights' type with contiguous rows, ids and fp32 weights packed")
         self.weights = weights
         G.gemm_moe_dispatch(T, K, self.groups, h, t, ids, X, X.stride(0), self.offsets, self.order,
                             self.pos, self.Xs, h, self.ws, id_bytes=ids.element_size())
@@ -78,6 +81,8 @@ class ExpertMLP:
         """dX, the gradient of the weights of the choices, dW1 and dW2 (fp32);
         accumulate: dW1 and dW2 are added to what they held."""
         T, K, n, h, f, t = self.tokens, self.topk, len(self.pos), self.hidden, self.inner, self.dtype
+        if dY.shape != (T, h) or dY.dtype != self.W1.dtype or dY.stride(1) != 1:
+            raise ValueError("dY is tokens x H in the weights' type with contiguous rows")
         G.gemm_moe_combine_backward(T, K, h, t, self.pos, self.weights, dY, dY.stride(0), self.Ys,
                                     h, n, self.dYs, h, self.dw)
         G.gemm_grouped_run(self.p_dh, self.dYs, self.W2, None, self.offsets, None, self.dH)
