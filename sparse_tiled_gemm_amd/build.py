@@ -10,6 +10,7 @@ import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -22,6 +23,8 @@ SOURCES = ["gemm_api.cpp", "kernels_dense.hip", "kernels_sparse.hip", "kernels_m
            "moe_api.cpp", "kernels_route.hip", "kernels_q8.hip", "kernels_grouped.hip",
            "kernels_grouped_rows.hip", "kernels_grouped_weights.hip",
            "kernels_grouped_skinny.hip"]
+
+PYCALL = os.path.join(HERE, "_pycall.so")  # csrc/pycall.c, the binding's call
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -53,6 +56,17 @@ def _compile(src, asm, verbose):
     return obj
 
 
+def _build_pycall(verbose):
+    """The CPython extension module the binding calls the C ABI through."""
+    tmp = PYCALL + ".tmp"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC",
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "pycall.c"), "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, PYCALL)
+
+
 def _stale(src):
     """True when src's object is missing or older than src or any header."""
     obj = os.path.join(BUILD, src + ".o")
@@ -66,9 +80,10 @@ def _stale(src):
 
 
 def build(verbose=False, asm=False, incremental=False):
-    """Compile every source (incremental=True: only those whose object is
+    """Compile every source and the binding's call (incremental=True: only those whose object is
     older than the source or a header) and link libstgemm.so."""
     os.makedirs(BUILD, exist_ok=True)
+    _build_pycall(verbose)
     todo = [s for s in SOURCES if not incremental or asm or _stale(s)]
     if todo:
         with concurrent.futures.ThreadPoolExecutor(max_workers=len(todo)) as ex:

@@ -39,6 +39,12 @@
 //
 // An 8-bit B (codes and scales of a checkpoint) is loaded into registers
 // instead, and brought to 16 bits and stored to LDS four clusters later.
+//
+// Measured on MI355X (256 x 256 tiles, bf16): one group of 8192^3 1500
+// TFLOP/s; rows, 16 groups of 16384 x 4096 x 4096, 483 us, 1138 TFLOP/s (matrix
+// pipe busy 65 %, of which the last round of tiles and the padding of ragged
+// groups cost about a fifth); weights, 16 groups of 4096 x 2048 fp32 added to
+// C over 16384 rows, 397 us (260 without the output), from 8 bits 413 us.
 #pragma once
 #include "grouped_common.hpp"
 

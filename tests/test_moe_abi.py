@@ -195,3 +195,20 @@ def test_q8_refusals(fn, args, status):
                        (dict(cols=-2), G.GEMM_ERR_INVALID_VALUE),
                        (dict(rows=1 << 40), G.GEMM_ERR_INVALID_VALUE)]:
         assert _status(fn, *dict(a, **change).values()) == st
+
+
+def test_arguments_of_the_wrong_kind():
+    """Integers, addresses, None and tensors only; nothing is cut to an integer."""
+    from sparse_tiled_gemm_amd import _pycall
+    torch = pytest.importorskip("torch")
+    a = dict(COMBINE, tokens=0, rows=0)
+    x = torch.zeros(4)
+    assert _status(G.gemm_moe_combine, *dict(a, pos=x, weights=x, Ys=x, Y=x).values()) == G.GEMM_OK
+    for k, v in [("tokens", 2.0), ("pos", "0"), ("weights", [1.0]), ("Ys", b"")]:
+        with pytest.raises(TypeError):
+            G.gemm_moe_combine(*dict(a, **{k: v}).values(), stream=0)
+    for bad in [(), ("f",), (1,) * 22]:
+        with pytest.raises(TypeError):
+            _pycall.call(*bad)
+    with pytest.raises(ValueError):
+        _pycall.call(0, 1)
