@@ -376,50 +376,62 @@ static bool grouped_tiled_ok(const gemm_grouped_desc_t &d)
 static int choose_family(const gemm_grouped_desc_t &d, int num_cu)
 {
     if (d.mode == GEMM_GROUPED_WEIGHTS) {
-        // While 64 x 64 tiles fit the chip at once (two per compute unit) a
+        // While 64 x 64 tiles fit the chip (three per compute unit at once) a
         // tile's way through the rows is the time: 4 groups of 3400 rows, 704
         // x 480, 34 with 64, 68 with 128; 2048 x 1024, 65 and 59.  The same
         // for 128 against 256: 4 groups of 2048 rows, 2048 x 1024, 57 and 75;
-        // 2048 x 4096, 199 and 144.
+        // 3 of 1200, 5904 x 448, 67 and 85; 2048 x 4096, 199 and 144.
         const int64_t t64 = d.groups * ceil_div(d.K, 64) * ceil_div(d.N, 64);
         const int64_t t128 = d.groups * ceil_div(d.K, 128) * ceil_div(d.N, 128);
         const int64_t t256 = d.groups * ceil_div(d.K, 256) * ceil_div(d.N, 256);
-        if (t64 <= 2 * num_cu)
+        if (t64 <= 3 * num_cu)
             return GF_TILED_64;
-        if (t128 <= 2 * num_cu)
-            return GF_TILED_128;
+        // (Where K or N ends in the first half of a 128 and has few, 64 wastes
+        // less: 8 groups of 1320 rows, 1032 x 264, 31 and 51.)
+        if (t128 <= 3 * num_cu)
+            return t64 * 10 <= t128 * 24 ? GF_TILED_64 : GF_TILED_128;
         // Many tiles: 256 moves less per product, 128 wastes less at the
         // edges and, two to a compute unit, hides its stores better, which
         // counts where the groups are short: 40 groups of 365 rows, 2136 x
-        // 384, 116 and 92; 17 groups of 36 rows, 488 x 3720, 50 and 47 (16 of
-        // 62 rows, 4096 x 2048, whole cache lines: 196 and 254); 3 groups of
-        // 1400, 6400 x 1240, 110 and 137.
-        if (d.rows >= 512 * (int64_t)d.groups)
-            return t256 * 3 <= t128 ? GF_TILED_256 : GF_TILED_128; // 4/3 of the area
+        // 384, 116 and 92; 11 of 285, 2952 x 1352, 78 and 67; 17 groups of 36
+        // rows, 488 x 3720, 50 and 47 (16 of 62 rows, 4096 x 2048, whole cache
+        // lines: 196 and 254); 3 groups of 1400, 6400 x 1240, 110 and 137.
         const bool lines = d.ldd * (d.d_type == GEMM_F32 ? 4 : 2) % 128 == 0;
-        return lines && t256 * 40 <= t128 * 11 ? GF_TILED_256 : GF_TILED_128;
+        return (lines || d.rows >= 256 * (int64_t)d.groups) && t256 * 33 <= t128 * 10
+                   ? GF_TILED_256
+                   : GF_TILED_128; // at most 6/5 of the area
     }
     // Rows: groups that can have rows, and the row tiles expected of them
     // (each wastes half a tile).
     const int64_t g = d.groups < d.rows ? d.groups : d.rows;
     auto expect = [&](int64_t b) { return (d.rows / b + (g + 1) / 2) * ceil_div(d.N, b); };
     // Few tiles: time is one workgroup's way through K.  Up to 16 rows per
-    // group the skinny kernel, whose waves split K (4 groups, 1024 x 2048: 4
-    // rows 6.0 against 9.6, 16 rows 7.2 and 9.7, 64 rows 9.7 and 9.8), then 64
-    // x 64 tiles (367 rows, 352 x 4880, 24 against 45 with 128; 6 groups of
-    // 324, 1072 x 1616, 26 and 25).
+    // group and 64 tiles the skinny kernel, whose waves split K (4 groups, 1024
+    // x 2048: 4 rows 6.0 against 9.6, 16 rows 7.2 and 9.7, 64 rows 9.7 and 9.8;
+    // 38 groups, 272 x 288, 3.9 and 4.9; past those its strips of 32 columns no
+    // longer run at once: 6 groups, 2520 x 264, 11.1 and 5.0), else 64 x 64
+    // tiles (367 rows, 352 x 4880, 24 against 45 with 128; 6 groups of 324,
+    // 1072 x 1616, 26 and 25).
     if (expect(64) <= 2 * num_cu)
-        return d.rows <= 16 * g ? GF_SKINNY : GF_TILED_64;
+        return d.rows <= 16 * g && expect(64) * 4 <= num_cu ? GF_SKINNY : GF_TILED_64;
     // Few rows per group: bound by B's stream.  32 groups, 4096 x 2048, with
     // 64 / 128 / 256: 4 rows each 109 / 123 / 122, 16 rows 114 / 125 / 132, 32
     // rows 131 / 132 / 135; row-major B, read in runs of a tile's width: 2
-    // rows 84 / 89 / 88, 4 rows 110 / 109 / 99, 16 rows 131 / 138 / 108.
-    if (d.rows < 32 * g)
-        return d.b_layout == GEMM_ROW_MAJOR && d.rows >= 4 * g ? GF_TILED_256 : GF_TILED_64;
+    // rows 84 / 89 / 88, 4 rows 110 / 109 / 99, 16 rows 131 / 138 / 108, but
+    // only while the last round of 256-wide tiles is mostly full: 27 groups of
+    // 16 rows, K 4096, N 2048 (216 tiles) 95 / 99 / 86, N 2816 (297) 125 / 137
+    // / 154, N 1048 (135) 58 / 55 / 74.
+    if (d.rows < 32 * g) {
+        const int64_t t = g * ceil_div(d.N, 256);
+        return d.b_layout == GEMM_ROW_MAJOR && d.rows >= 4 * g &&
+                       t * 5 >= ceil_div(t, num_cu) * num_cu * 4
+                   ? GF_TILED_256
+                   : GF_TILED_64;
+    }
     // 8 groups of 256 rows, 2048 x 1024, 19 with 128 and 20 with 256, x 4096
     // 77 and 67; 15 groups of 208, 1504 x 408, 15 and 17; 8 of 1024, 2048 x
-    // 1024, 52 and 47.
-    return expect(128) <= (d.K <= 1024 ? 2 : 1) * (int64_t)num_cu ? GF_TILED_128 : GF_TILED_256;
+    // 1024, 52 and 47; 4 of 800, 2472 x 136, 15 and 18.
+    return expect(128) <= (d.K <= 512 ? 3 : 1) * (int64_t)num_cu ? GF_TILED_128 : GF_TILED_256;
 }
 
 static const char *grouped_family_name(int f)
