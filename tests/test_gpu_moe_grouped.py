@@ -272,3 +272,75 @@ def test_forced_algorithms(algo):
             G.gemm_grouped_plan(d("weights"))
     else:
         assert algo in G.gemm_grouped_plan(d("weights")).name
+
+
+def _far(gen, rows, cols, ld, off=8):
+    """rows x cols of a matrix of several GiB, NaN beside them."""
+    buf = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda")
+    v = buf.view(rows, ld)
+    v[:, :off + cols + 256] = float("nan")
+    v[:, off:off + cols] = torch.randn(rows, cols, generator=gen).bfloat16()
+    return v[:, off:off + cols]
+
+
+@pytest.mark.parametrize("algo", FAMILIES)
+def test_offsets_past_32_bits(algo):
+    """Operands of 4.8 GB each: a group's last K rows lie past 2^32 bytes of
+    its first, and its rows past 2^32 bytes of the operand's."""
+    say("far", algo)
+    gen = torch.Generator().manual_seed(9)
+    rows, ld, offsets = 2400, 1000000, [0, 3, 2397]
+    off_d = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    A, B = _far(gen, rows, 72, ld), _far(gen, rows, 136, ld)
+    if algo != "skinny":
+        plan = _plan(algo, "weights", rows, 136, 72, 2, "bf16", "bf16", "f32", lda=ld, ldb=ld)
+        D = torch.empty(2, 72, 136, device="cuda")
+        G.gemm_grouped_run(plan, A, B, None, off_d, None, D)
+        torch.cuda.synchronize()
+        ref, S = R.weights_ref(A.cpu(), B.cpu(), offsets)
+        bound = R.half_step("f32", ref) * 1.001 + rows * 2 * R.U32 * S
+        assert ((D.cpu().double() - ref).abs() <= bound).all(), plan.name
+    # rows: B is one group's 2400 x 136 (row-major), A's rows a pitch of ld apart
+    offsets = [3, 2397]
+    X = A[:, :72]
+    W = torch.randn(136, 72, generator=gen).bfloat16()
+    plan = _plan(algo, "rows", rows, 136, 72, 1, "bf16", "bf16", "f32", lda=ld)
+    D = torch.zeros(rows, 136, device="cuda")
+    off_d = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    G.gemm_grouped_run(plan, X, W.cuda(), None, off_d, None, D)
+    torch.cuda.synchronize()
+    _, ref, S = R.rows_ref(X.cpu(), W[None], offsets, "col")[0]
+    bound = R.half_step("f32", ref) * 1.001 + 74 * 2 * R.U32 * S
+    assert ((D.cpu()[3:2397].double() - ref).abs() <= bound).all(), plan.name
+    Y = torch.randn(40, rows, generator=gen).bfloat16()
+    plan = _plan(algo, "rows", 40, 136, rows, 1, "bf16", "bf16", "f32", b_layout="row", ldb=ld)
+    D = torch.zeros(40, 136, device="cuda")
+    off_d = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    G.gemm_grouped_run(plan, Y.cuda(), B, None, off_d, None, D)
+    torch.cuda.synchronize()
+    _, ref, S = R.rows_ref(Y, B.cpu()[None], [0, 40], "row")[0]
+    bound = R.half_step("f32", ref) * 1.001 + (rows + 2) * 2 * R.U32 * S
+    assert ((D.cpu().double() - ref).abs() <= bound).all(), plan.name
+
+
+@pytest.mark.parametrize("algo", ["auto", "tiled64", "tiled128", "tiled256"])
+def test_codes_past_32_bits(algo):
+    """4.4 GB of 8-bit codes: the first and last columns of the product."""
+    say("far codes", algo)
+    gen = torch.Generator().manual_seed(10)
+    dgen = torch.Generator(device="cuda").manual_seed(10)
+    rows, N, K, offsets = 4400, 1000000, 8, [0, 4400]
+    plan = _plan(algo, "weights", rows, N, K, 1, "bf16", "e4m3", "f32")
+    A = torch.randn(rows, K, generator=gen).bfloat16()
+    B = torch.randint(0, 0x78, (rows, N), generator=dgen, dtype=torch.uint8, device="cuda")
+    scales = torch.randint(118, 128, (rows, N // 32), generator=dgen, dtype=torch.uint8,
+                           device="cuda")
+    D = torch.empty(1, K, N, device="cuda")
+    off_d = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    G.gemm_grouped_run(plan, A.cuda(), B, scales, off_d, None, D)
+    torch.cuda.synchronize()
+    for c in (0, N - 192):
+        Bv = R.q8_load_ref(B[:, c:c + 192].cpu(), scales[:, c // 32:c // 32 + 6].cpu(), "bf16")
+        ref, S = R.weights_ref(A, Bv, offsets)
+        bound = R.half_step("f32", ref) * 1.001 + rows * 2 * R.U32 * S
+        assert ((D[:, :, c:c + 192].cpu().double() - ref).abs() <= bound).all(), plan.name
