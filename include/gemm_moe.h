@@ -195,7 +195,8 @@ gemm_status_t gemm_swiglu(int64_t rows, int64_t cols, int32_t type, const void *
  * s = 1 / (1 + exp(-g)):
  *   dG = dH * u * s * (1 + g (1 - s)),  dU = dH * g * s   (dGU: rows x 2 cols)
  * and H = silu(g) * u once more, which the gradient of the next weights
- * reads (NULL: not wanted). */
+ * reads (NULL: not wanted).  g and u are the codes' values clamped to the
+ * type's finite range. */
 gemm_status_t gemm_swiglu_backward(int64_t rows, int64_t cols, int32_t type, const uint8_t *codes,
                                    const uint8_t *scales, const void *dH, int64_t lddh, void *dGU,
                                    int64_t lddgu, void *H, int64_t ldh, gemm_stream_t stream);

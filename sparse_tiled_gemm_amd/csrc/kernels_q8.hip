@@ -214,6 +214,8 @@ __global__ __launch_bounds__(256) void k_q8_load(Q8Args a)
 
 // ---------------------------------------------------------------- backward
 
+// The values are clamped to the type's range, as in k_q8_load: the block that
+// ends at bfloat16's largest value has codes of 256 * 2^120, infinity in fp32.
 template <bool BF, int TPR>
 __global__ __launch_bounds__(256) void k_swiglu_backward(Q8Args a)
 {
@@ -235,6 +237,8 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(Q8Args a)
             widen8<BF>(dv, d);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+                g[e] = clamp16<BF>(g[e]);
+                u[e] = clamp16<BF>(u[e]);
                 const float s = sigmoid(g[e]), gs = g[e] * s;
                 dg[e] = d[e] * u[e] * s * (1.0f + g[e] * (1.0f - s));
                 du[e] = d[e] * gs;

@@ -181,3 +181,36 @@ def test_backward_against_differences():
     tol = lambda x: R.half_step("f16", x) * 1.01 + 1e-6 * (1 + (u * dH.double()).abs())
     assert ((got[:, :cols] - dg).abs() <= tol(dg)).all()
     assert ((got[:, cols:] - du).abs() <= tol(du)).all()
+
+
+def _backward(GU, dH, dtype):
+    """Codes of GU, the clamped values they stand for, and dG, dU, H (64 bits, CPU)."""
+    rows, cols = dH.shape
+    codes, scales = _store(GU)
+    dGU = torch.empty(rows, 2 * cols, dtype=R.DT[dtype], device="cuda")
+    H = torch.empty(rows, cols, dtype=R.DT[dtype], device="cuda")
+    G.gemm_swiglu_backward(rows, cols, dtype, codes.cuda(), scales.cuda(), dH.cuda(), 0, dGU, 0, H, 0)
+    torch.cuda.synchronize()
+    v = R.q8_load_ref(codes, scales, dtype).double()
+    d = dGU.cpu().double()
+    return v[:, :cols], v[:, cols:], (d[:, :cols], d[:, cols:], H.cpu().double())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_backward_at_the_end_of_the_range(dtype):
+    """Finite inputs whose code times its scale lies past the type's range
+    (bfloat16: past fp32's as well) enter as the type's largest value."""
+    big = torch.finfo(R.DT[dtype]).max
+    pairs = [(big, 0.5), (big, -0.25), (0.97 * big, 0.5), (-big, 2.0), (1.0, big), (-2.0, big),
+             (-2.0, -0.98 * big), (0.0, big), (0.0, -big)]
+    cols = 64
+    X = torch.tensor(pairs).repeat_interleave(cols, 1).to(R.DT[dtype])  # a value per block
+    dH = torch.full((len(pairs), cols), 2.0 ** -10).to(R.DT[dtype])
+    g, u, got = _backward(X, dH, dtype)
+    refs, bounds = R.swiglu_backward_ref(g, u, dH.double())
+    for x, want, b in zip(got, refs, bounds):
+        # far gates: sigmoid is 0 or 1 to the last bit, and each result is at
+        # most four fp32 roundings of its products away
+        b = torch.where(g.abs() > 100, 4 * R.U32 * want.abs(), b)
+        assert torch.isfinite(x).all()
+        assert ((x - want).abs() <= R.half_step(dtype, want) * 1.001 + b).all()
