@@ -240,7 +240,10 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(Q8Args a)
                 g[e] = clamp16<BF>(g[e]);
                 u[e] = clamp16<BF>(u[e]);
                 const float s = sigmoid(g[e]), gs = g[e] * s;
-                dg[e] = d[e] * u[e] * s * (1.0f + g[e] * (1.0f - s));
+                // (dH * u may leave fp32's range where s brings it back: both
+                // are above 1 then, and the gate's derivative goes first)
+                const float p = d[e] * u[e], k = 1.0f + g[e] * (1.0f - s);
+                dg[e] = __builtin_fabsf(p) < __builtin_inff() ? p * s * k : d[e] * (s * k) * u[e];
                 du[e] = d[e] * gs;
                 h[e] = gs * u[e];
             }

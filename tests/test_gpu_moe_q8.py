@@ -214,3 +214,24 @@ def test_backward_at_the_end_of_the_range(dtype):
         b = torch.where(g.abs() > 100, 4 * R.U32 * want.abs(), b)
         assert torch.isfinite(x).all()
         assert ((x - want).abs() <= R.half_step(dtype, want) * 1.001 + b).all()
+
+
+def test_backward_products_that_overflow_on_the_way():
+    """dH * u past fp32's range where the gate brings dG back into it."""
+    cols = 32
+    cases = [  # g, u, dH
+        (-200.0, 1e35, 1e5), (-200.0, -1e35, 1e5), (-40.0, 1e20, 1e20), (-30.0, 1e24, -1e22),
+        (-30.0, 1e22, 1e24), (-3e38, 1e30, 1e30), (-20.0, 3e38, 30.0)]
+    t = torch.tensor(cases).bfloat16()
+    X = t[:, :2].repeat_interleave(cols, 1)
+    dH = t[:, 2:].repeat_interleave(cols, 1)
+    g, u, (dg, du, h) = _backward(X, dH, "bf16")
+    (rg, _, _), (bg, _, _) = R.swiglu_backward_ref(g, u, dH.double())
+    bg = torch.where(g < -100, torch.zeros_like(bg), bg)  # the gate is zero
+    rg = torch.where(g < -100, torch.zeros_like(rg), rg)
+    assert (rg.abs() < torch.finfo(torch.bfloat16).max).all()
+    assert ((dg - rg).abs() <= R.half_step("bf16", rg) * 1.001 + bg).all()
+    # and past the type's range where it does not
+    X = torch.tensor([[50.0, -1e20]]).bfloat16().repeat_interleave(cols, 1)
+    _, _, (dg, _, _) = _backward(X, torch.full((1, cols), 1e20).bfloat16(), "bf16")
+    assert (dg == -float("inf")).all()
