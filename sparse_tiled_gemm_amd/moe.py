@@ -21,6 +21,16 @@ from . import gemm as G
 _NAME = {torch.float16: "f16", torch.bfloat16: "bf16"}
 
 
+def _rows(x):
+    """x (rows with contiguous elements) and its leading dimension.  Rows that
+    share memory (one row broadcast to all: a stride of 0, which the library
+    takes for "packed") are copied out; a single row's stride means nothing."""
+    rows, cols = x.shape
+    if rows > 1 and x.stride(0) < cols:
+        x = x.contiguous()
+    return x, x.stride(0) if rows > 1 else cols
+
+
 class ExpertMLP:
     def __init__(self, W1, W2, tokens, topk):
         self.groups, two_f, self.hidden = W1.shape
@@ -66,7 +76,8 @@ class ExpertMLP:
                 not (ids.is_contiguous() and weights.is_contiguous()):
             raise ValueError("X in the weights' type with contiguous rows, ids and fp32 weights packed")
         self.weights = weights
-        G.gemm_moe_dispatch(T, K, self.groups, h, t, ids, X, X.stride(0), self.offsets, self.order,
+        X, ldx = _rows(X)
+        G.gemm_moe_dispatch(T, K, self.groups, h, t, ids, X, ldx, self.offsets, self.order,
                             self.pos, self.Xs, h, self.ws, id_bytes=ids.element_size())
         G.gemm_grouped_run(self.p_up, self.Xs, self.W1, None, self.offsets, None, self.GU)
         G.gemm_swiglu(n, f, t, self.GU, 2 * f, self.H, f, self.codes, self.scales)
@@ -83,8 +94,9 @@ class ExpertMLP:
         T, K, n, h, f, t = self.tokens, self.topk, len(self.pos), self.hidden, self.inner, self.dtype
         if dY.shape != (T, h) or dY.dtype != self.W1.dtype or dY.stride(1) != 1:
             raise ValueError("dY is tokens x H in the weights' type with contiguous rows")
-        G.gemm_moe_combine_backward(T, K, h, t, self.pos, self.weights, dY, dY.stride(0), self.Ys,
-                                    h, n, self.dYs, h, self.dw)
+        dY, lddy = _rows(dY)
+        G.gemm_moe_combine_backward(T, K, h, t, self.pos, self.weights, dY, lddy, self.Ys, h, n,
+                                    self.dYs, h, self.dw)
         G.gemm_grouped_run(self.p_dh, self.dYs, self.W2, None, self.offsets, None, self.dH)
         G.gemm_swiglu_backward(n, f, t, self.codes, self.scales, self.dH, f, self.dGU, 2 * f,
                                self.H, f)

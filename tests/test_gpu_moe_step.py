@@ -119,3 +119,22 @@ def test_other_stream_and_graph():
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_strides_of_rows(tokens):
+    """Padded, broadcast and overlapping rows give what packed copies give."""
+    p = _problem(tokens, 64, 32, 4, 2, torch.bfloat16, 5)
+    layer = moe.ExpertMLP(p[4].cuda(), p[5].cuda(), tokens, 2)
+    X, ids, w, dY = p[0].cuda(), p[3].cuda(), p[2].cuda(), p[1].cuda()
+    wide = torch.full((tokens, 72), 9.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, :64] = X
+    lapped = torch.randn(64 + 3 * tokens, device="cuda").bfloat16()
+    for x, dy in [(wide[:, :64], dY), (X, wide[:, :64]), (X[:1].expand(tokens, 64), dY),
+                  (X, dY[:1].expand(tokens, 64)), (lapped.as_strided((tokens, 64), (3, 1)), dY)]:
+        say("strides", x.stride(), dy.stride())
+        step = lambda x_, dy_: [t.clone() for t in (layer.forward(x_, ids, w),) + layer.backward(dy_)]
+        got, want = step(x, dy), step(x.clone().contiguous(), dy.clone().contiguous())
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

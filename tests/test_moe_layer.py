@@ -1,0 +1,99 @@
+"""The layer's handling of its arguments (sparse_tiled_gemm_amd.moe), without
+a GPU: the library's calls are recorded instead of made, with the tensors and
+leading dimensions that the kernels would have read."""
+import types
+
+import pytest
+import torch
+
+from sparse_tiled_gemm_amd import gemm as G
+from sparse_tiled_gemm_amd import moe
+
+T, K, E, H, F = 5, 2, 3, 16, 8
+
+
+class Recorded(types.SimpleNamespace):
+    def __init__(self):
+        super().__init__(calls=[], make_grouped_desc=G.make_grouped_desc,
+                         gemm_moe_sort_workspace=lambda *a: 0,
+                         gemm_grouped_plan=lambda desc: types.SimpleNamespace(desc=desc))
+        for name in ("gemm_moe_dispatch", "gemm_grouped_run", "gemm_swiglu", "gemm_moe_combine",
+                     "gemm_q8_store", "gemm_moe_combine_backward", "gemm_swiglu_backward"):
+            setattr(self, name, lambda *a, _n=name, **kw: self.calls.append((_n, a, kw)))
+
+    def args(self, name):
+        return [a for n, a, _ in self.calls if n == name][-1]
+
+
+class OnDevice(torch.Tensor):
+    """A tensor in host memory that says it is on the device."""
+    is_cuda = True
+
+
+def dev(x):
+    return x.as_subclass(OnDevice)
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    lib = Recorded()
+    monkeypatch.setattr(moe, "G", lib)
+    return lib
+
+
+def layer_of(tokens=T):
+    return moe.ExpertMLP(dev(torch.zeros(E, 2 * F, H, dtype=torch.bfloat16)),
+                         dev(torch.zeros(E, H, F, dtype=torch.bfloat16)), tokens, K)
+
+
+def inputs(tokens=T):
+    gen = torch.Generator().manual_seed(0)
+    return (dev(torch.randn(tokens, H, generator=gen).bfloat16()),
+            dev(torch.randint(0, E, (tokens, K), generator=gen)),
+            dev(torch.rand(tokens, K, generator=gen)))
+
+
+def read_back(x, ld, rows, cols):
+    """What a kernel reads at x with leading dimension ld (0: packed)."""
+    ld = ld or cols
+    assert ld >= cols
+    last = x.storage_offset() + (rows - 1) * ld + cols
+    assert last * x.element_size() <= x.untyped_storage().nbytes(), "read past the buffer"
+    return x.as_strided((rows, cols), (ld, 1))
+
+
+def views(x):
+    """The same rows in other strides."""
+    wide = torch.zeros(len(x), H + 8, dtype=x.dtype)
+    wide[:, :H] = x
+    row = x[:1]
+    lapped = torch.arange(H + 3 * T, dtype=x.dtype)
+    return {"packed": x, "padded": dev(wide[:, :H]), "every other": dev(x.repeat_interleave(2, 0)[::2]),
+            "one row": row.expand(len(x), H),
+            "overlapping": dev(lapped.as_strided((len(x), H), (3, 1)))}
+
+
+@pytest.mark.parametrize("kind", ["packed", "padded", "every other", "one row", "overlapping"])
+def test_rows_are_read_where_they_lie(lib, kind):
+    """X and dY of any row stride, broadcast rows among them."""
+    layer, (X, ids, w) = layer_of(), inputs()
+    x = views(X)[kind]
+    layer.forward(x, ids, w)
+    a = lib.args("gemm_moe_dispatch")
+    assert torch.equal(read_back(a[6], a[7], T, H), x)
+    layer.backward(x)
+    a = lib.args("gemm_moe_combine_backward")
+    assert torch.equal(read_back(a[6], a[7], T, H), x)
+
+
+def test_one_token_of_any_stride(lib):
+    """The row stride of a single row means nothing."""
+    layer, (X, ids, w) = layer_of(1), inputs(1)
+    for stride in (1, 0, H - 1, 1000):
+        x = dev(X.as_strided((1, H), (stride, 1)))
+        layer.forward(x, ids, w)
+        a = lib.args("gemm_moe_dispatch")
+        assert torch.equal(read_back(a[6], a[7], 1, H), x)
+        layer.backward(x)
+        a = lib.args("gemm_moe_combine_backward")
+        assert torch.equal(read_back(a[6], a[7], 1, H), x)
