@@ -31,6 +31,13 @@ def _rows(x):
     return x, x.stride(0) if rows > 1 else cols
 
 
+def _check_device(device, **tensors):
+    """The library takes addresses: what lies elsewhere would fault in a kernel."""
+    for name, x in tensors.items():
+        if not x.is_cuda or x.device != device:
+            raise ValueError("%s has to lie on the weights' GPU" % name)
+
+
 class ExpertMLP:
     def __init__(self, W1, W2, tokens, topk):
         self.groups, two_f, self.hidden = W1.shape
@@ -38,6 +45,7 @@ class ExpertMLP:
         if W2.shape != (self.groups, self.hidden, self.inner) or W1.dtype != W2.dtype or \
                 two_f % 2 or W1.dtype not in _NAME:
             raise ValueError("W1 (experts x 2F x H) and W2 (experts x H x F) in f16 or bf16")
+        _check_device(W1.device, W1=W1, W2=W2)
         self.W1, self.W2 = W1.contiguous(), W2.contiguous()
         self.tokens, self.topk = tokens, topk
         dt, dev = W1.dtype, W1.device
@@ -75,6 +83,7 @@ class ExpertMLP:
         if X.dtype != self.W1.dtype or X.stride(1) != 1 or weights.dtype != torch.float32 or \
                 not (ids.is_contiguous() and weights.is_contiguous()):
             raise ValueError("X in the weights' type with contiguous rows, ids and fp32 weights packed")
+        _check_device(self.W1.device, X=X, ids=ids, weights=weights)
         self.weights = weights
         X, ldx = _rows(X)
         G.gemm_moe_dispatch(T, K, self.groups, h, t, ids, X, ldx, self.offsets, self.order,
@@ -94,6 +103,7 @@ class ExpertMLP:
         T, K, n, h, f, t = self.tokens, self.topk, len(self.pos), self.hidden, self.inner, self.dtype
         if dY.shape != (T, h) or dY.dtype != self.W1.dtype or dY.stride(1) != 1:
             raise ValueError("dY is tokens x H in the weights' type with contiguous rows")
+        _check_device(self.W1.device, dY=dY)
         dY, lddy = _rows(dY)
         G.gemm_moe_combine_backward(T, K, h, t, self.pos, self.weights, dY, lddy, self.Ys, h, n,
                                     self.dYs, h, self.dw)

@@ -97,3 +97,28 @@ def test_one_token_of_any_stride(lib):
         layer.backward(x)
         a = lib.args("gemm_moe_combine_backward")
         assert torch.equal(read_back(a[6], a[7], 1, H), x)
+
+
+def test_tensors_off_the_device_are_refused(lib):
+    """Host memory never reaches a kernel."""
+    W1, W2 = torch.zeros(E, 2 * F, H).bfloat16(), torch.zeros(E, H, F).bfloat16()
+    for a, b in [(W1, W2), (dev(W1), W2), (W1, dev(W2))]:
+        with pytest.raises(ValueError):
+            moe.ExpertMLP(a, b, T, K)
+    layer, (X, ids, w) = layer_of(), inputs()
+    host = [t.as_subclass(torch.Tensor) for t in (X, ids, w)]
+    meta = [torch.empty_like(t, device="meta") for t in host]  # another device
+    lib.calls.clear()
+    for i in range(3):
+        for other in (host, meta):
+            a = [X, ids, w]
+            a[i] = other[i]
+            with pytest.raises(ValueError):
+                layer.forward(*a)
+    assert not lib.calls
+    layer.forward(X, ids, w)
+    lib.calls.clear()
+    for dY in (host[0], meta[0]):
+        with pytest.raises(ValueError):
+            layer.backward(dY)
+    assert not lib.calls
