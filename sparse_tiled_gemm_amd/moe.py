@@ -6,8 +6,8 @@ include/gemm_moe.h: the path that runs them together.
     dX, dweights, dW1, dW2 = layer.backward(dY)
 
 W1 (experts x 2F x H) holds each expert's gate and up projection, W2 (experts
-x H x F) its down projection; X is tokens x H, ids (int64) and weights (fp32)
-are tokens x topk, an id out of range drops its slot.  All buffers are made
+x H x F) its down projection; X is tokens x H, ids (int32 or int64) and
+weights (fp32) are tokens x topk, an id out of range drops its slot.  All buffers are made
 once; a step only enqueues kernels, so it may be captured into a HIP graph.
 
 Between the passes the layer keeps the input of the activation in 8 bits
@@ -83,6 +83,8 @@ class ExpertMLP:
         if X.dtype != self.W1.dtype or X.stride(1) != 1 or weights.dtype != torch.float32 or \
                 not (ids.is_contiguous() and weights.is_contiguous()):
             raise ValueError("X in the weights' type with contiguous rows, ids and fp32 weights packed")
+        if ids.dtype not in (torch.int32, torch.int64):
+            raise ValueError("ids in int32 or int64")
         _check_device(self.W1.device, X=X, ids=ids, weights=weights)
         self.weights = weights
         X, ldx = _rows(X)

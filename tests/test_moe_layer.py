@@ -122,3 +122,15 @@ def test_tensors_off_the_device_are_refused(lib):
         with pytest.raises(ValueError):
             layer.backward(dY)
     assert not lib.calls
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64, torch.int16, torch.uint8, torch.bool])
+def test_ids_of_another_type_are_refused(lib, dtype):
+    """Floats of an integer's size are not read as its bits."""
+    layer, (X, ids, w) = layer_of(), inputs()
+    with pytest.raises(ValueError):
+        layer.forward(X, dev(ids.to(dtype)), w)
+    assert not lib.calls
+    for ok, size in ((torch.int32, 4), (torch.int64, 8)):
+        layer.forward(X, dev(ids.to(ok)), w)
+        assert [kw for n, _, kw in lib.calls if n == "gemm_moe_dispatch"][-1]["id_bytes"] == size
