@@ -54,7 +54,7 @@ class ExpertMLP:
         mk = lambda *s, d=dt: torch.empty(s, dtype=d, device=dev)
         i32, u8, f32 = torch.int32, torch.uint8, torch.float32
         # rows past the last group are never written: zeros keep them finite
-        z = lambda *s: torch.zeros(s, dtype=dt, device=dev)
+        z = lambda *s, d=dt: torch.zeros(s, dtype=d, device=dev)
         self.offsets, self.order, self.pos = mk(g + 1, d=i32), mk(n, d=i32), mk(n, d=i32)
         self.ws = mk(max(G.gemm_moe_sort_workspace(tokens, topk, g), 1), d=u8)
         self.Xs, self.GU, self.H, self.Ys = z(n, h), z(n, 2 * f), z(n, f), z(n, h)
@@ -62,8 +62,8 @@ class ExpertMLP:
         self.xcodes, self.xscales = mk(n, h, d=u8), mk(n, (h + 31) // 32, d=u8)
         self.Y, self.dX, self.dw = mk(tokens, h), mk(tokens, h), mk(tokens, topk, d=f32)
         self.dYs, self.dH, self.dGU, self.dXs = z(n, h), z(n, f), z(n, 2 * f), z(n, h)
-        # (H x 2F) and (F x H): the weights' gradients, transposed against W1 and W2
-        self.dW1, self.dW2 = mk(g, 2 * f, h, d=f32), mk(g, h, f, d=f32)
+        # in W1's and W2's layout; zeros, so that the first step may accumulate
+        self.dW1, self.dW2 = z(g, 2 * f, h, d=f32), z(g, h, f, d=f32)
         plan = lambda *a, **k: G.gemm_grouped_plan(G.make_grouped_desc(*a, **k))
         self.p_up = plan("rows", n, 2 * f, h, g, t, t, t)
         self.p_down = plan("rows", n, h, f, g, t, t, t)

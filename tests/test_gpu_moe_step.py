@@ -138,3 +138,19 @@ def test_strides_of_rows(tokens):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_first_backward_may_accumulate():
+    p = _problem(40, 64, 32, 4, 2, torch.bfloat16, 6)
+    X, ids, w, dY = p[0].cuda(), p[3].cuda(), p[2].cuda(), p[1].cuda()
+    out = []
+    for accumulate in (False, True):
+        # what the allocator hands out next has been used
+        junk = [torch.full((n,), float("nan"), device="cuda") for n in (4 * 64 * 64, 4 * 64 * 32) * 2]
+        del junk
+        layer = moe.ExpertMLP(p[4].cuda(), p[5].cuda(), 40, 2)
+        layer.forward(X, ids, w)
+        out.append([t.clone() for t in layer.backward(dY, accumulate=accumulate)])
+    torch.cuda.synchronize()
+    for a, b in zip(*out):
+        assert torch.equal(a, b)

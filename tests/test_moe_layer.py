@@ -134,3 +134,13 @@ def test_ids_of_another_type_are_refused(lib, dtype):
     for ok, size in ((torch.int32, 4), (torch.int64, 8)):
         layer.forward(X, dev(ids.to(ok)), w)
         assert [kw for n, _, kw in lib.calls if n == "gemm_moe_dispatch"][-1]["id_bytes"] == size
+
+
+def test_weight_gradients_start_at_zero(lib):
+    """The first backward pass may accumulate."""
+    torch.use_deterministic_algorithms(True)  # torch.empty's memory is filled with NaN
+    try:
+        layer = layer_of()
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert (layer.dW1 == 0).all() and (layer.dW2 == 0).all()
