@@ -61,6 +61,9 @@ class ExpertMLP:
         self.codes, self.scales = mk(n, 2 * f, d=u8), mk(n, (2 * f + 31) // 32, d=u8)
         self.xcodes, self.xscales = mk(n, h, d=u8), mk(n, (h + 31) // 32, d=u8)
         self.Y, self.dX, self.dw = mk(tokens, h), mk(tokens, h), mk(tokens, topk, d=f32)
+        # the forward pass's own copy: the caller may change its tensor before
+        # the backward pass
+        self.weights = mk(tokens, topk, d=f32)
         self.dYs, self.dH, self.dGU, self.dXs = z(n, h), z(n, f), z(n, 2 * f), z(n, h)
         # in W1's and W2's layout; zeros, so that the first step may accumulate
         self.dW1, self.dW2 = z(g, 2 * f, h, d=f32), z(g, h, f, d=f32)
@@ -86,14 +89,14 @@ class ExpertMLP:
         if ids.dtype not in (torch.int32, torch.int64):
             raise ValueError("ids in int32 or int64")
         _check_device(self.W1.device, X=X, ids=ids, weights=weights)
-        self.weights = weights
+        self.weights.copy_(weights.detach())  # no graph of the caller's
         X, ldx = _rows(X)
         G.gemm_moe_dispatch(T, K, self.groups, h, t, ids, X, ldx, self.offsets, self.order,
                             self.pos, self.Xs, h, self.ws, id_bytes=ids.element_size())
         G.gemm_grouped_run(self.p_up, self.Xs, self.W1, None, self.offsets, None, self.GU)
         G.gemm_swiglu(n, f, t, self.GU, 2 * f, self.H, f, self.codes, self.scales)
         G.gemm_grouped_run(self.p_down, self.H, self.W2, None, self.offsets, None, self.Ys)
-        G.gemm_moe_combine(T, K, h, t, self.pos, weights, self.Ys, h, n, self.Y, h)
+        G.gemm_moe_combine(T, K, h, t, self.pos, self.weights, self.Ys, h, n, self.Y, h)
         self.keep8 = keep8
         if keep8:  # the sorted inputs wait for the backward pass in 8 bits
             G.gemm_q8_store(n, h, t, self.Xs, h, self.xcodes, self.xscales)

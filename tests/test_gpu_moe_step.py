@@ -154,3 +154,34 @@ def test_first_backward_may_accumulate():
     torch.cuda.synchronize()
     for a, b in zip(*out):
         assert torch.equal(a, b)
+
+
+def test_weights_changed_between_the_passes():
+    """backward() is the gradient of the forward pass that was run, eagerly and
+    from two graphs with the weights changed between their replays."""
+    p = _problem(40, 64, 32, 4, 2, torch.bfloat16, 7)
+    layer = moe.ExpertMLP(p[4].cuda(), p[5].cuda(), 40, 2)
+    X, ids, w, dY = p[0].cuda(), p[3].cuda(), p[2].cuda(), p[1].cuda()
+    layer.forward(X, ids, w)
+    want = [t.clone() for t in layer.backward(dY)]
+    layer.forward(X, ids, w)
+    w.mul_(3)
+    got = [t.clone() for t in layer.backward(dY)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    fwd, bwd = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(fwd):
+        layer.forward(X, ids, w)
+    with torch.cuda.graph(bwd):
+        out = layer.backward(dY)
+    for i in range(3):
+        w.copy_(p[2])
+        torch.cuda.synchronize()
+        fwd.replay()
+        w.fill_(float(i))
+        bwd.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+            a.fill_(5)

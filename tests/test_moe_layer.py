@@ -144,3 +144,19 @@ def test_weight_gradients_start_at_zero(lib):
     finally:
         torch.use_deterministic_algorithms(False)
     assert (layer.dW1 == 0).all() and (layer.dW2 == 0).all()
+
+
+def test_weights_are_kept_as_they_were(lib):
+    """The gradient is that of the forward pass, whatever the caller does to
+    the weights in between."""
+    layer, (X, ids, w) = layer_of(), inputs()
+    want = w.clone()
+    layer.forward(X, ids, w)
+    a = lib.args("gemm_moe_combine")
+    assert torch.equal(read_back(a[5].view(T, K), 0, T, K), want)
+    w.fill_(7)
+    layer.backward(X)
+    a = lib.args("gemm_moe_combine_backward")
+    assert torch.equal(read_back(a[5].view(T, K), 0, T, K), want)
+    layer.forward(X, ids, w.clone().requires_grad_(True))
+    assert not layer.weights.requires_grad
