@@ -76,7 +76,7 @@ class ExpertMLP:
                                       has_c=acc) for k8 in (False, True) for acc in (False, True)}
         self.p_dw2 = {acc: plan("weights", n, f, h, g, t, t, "f32", has_c=acc)
                       for acc in (False, True)}
-        self.keep8 = False
+        self.keep8 = None  # of the last forward pass; None: there was none
 
     def forward(self, X, ids, weights, keep8=False):
         """Y = sum over each token's experts of weight * W2 (silu(W1g x) * W1u x)."""
@@ -108,6 +108,8 @@ class ExpertMLP:
         T, K, n, h, f, t = self.tokens, self.topk, len(self.pos), self.hidden, self.inner, self.dtype
         if dY.shape != (T, h) or dY.dtype != self.W1.dtype or dY.stride(1) != 1:
             raise ValueError("dY is tokens x H in the weights' type with contiguous rows")
+        if self.keep8 is None:
+            raise RuntimeError("backward before the first forward")
         _check_device(self.W1.device, dY=dY)
         dY, lddy = _rows(dY)
         G.gemm_moe_combine_backward(T, K, h, t, self.pos, self.weights, dY, lddy, self.Ys, h, n,

@@ -160,3 +160,13 @@ def test_weights_are_kept_as_they_were(lib):
     assert torch.equal(read_back(a[5].view(T, K), 0, T, K), want)
     layer.forward(X, ids, w.clone().requires_grad_(True))
     assert not layer.weights.requires_grad
+
+
+def test_backward_needs_a_forward(lib):
+    layer, (X, ids, w) = layer_of(), inputs()
+    with pytest.raises(RuntimeError):
+        layer.backward(X)
+    assert not lib.calls
+    layer.forward(X, ids, w)
+    layer.backward(X)
+    layer.backward(X)  # of the same forward pass once more
