@@ -97,8 +97,8 @@ class ExpertMLP:
         G.gemm_swiglu(n, f, t, self.GU, 2 * f, self.H, f, self.codes, self.scales)
         G.gemm_grouped_run(self.p_down, self.H, self.W2, None, self.offsets, None, self.Ys)
         G.gemm_moe_combine(T, K, h, t, self.pos, self.weights, self.Ys, h, n, self.Y, h)
-        self.keep8 = keep8
-        if keep8:  # the sorted inputs wait for the backward pass in 8 bits
+        self.keep8 = bool(keep8)
+        if self.keep8:  # the sorted inputs wait for the backward pass in 8 bits
             G.gemm_q8_store(n, h, t, self.Xs, h, self.xcodes, self.xscales)
         return self.Y
 
@@ -111,6 +111,7 @@ class ExpertMLP:
         if self.keep8 is None:
             raise RuntimeError("backward before the first forward")
         _check_device(self.W1.device, dY=dY)
+        accumulate = bool(accumulate)
         dY, lddy = _rows(dY)
         G.gemm_moe_combine_backward(T, K, h, t, self.pos, self.weights, dY, lddy, self.Ys, h, n,
                                     self.dYs, h, self.dw)

@@ -170,3 +170,13 @@ def test_backward_needs_a_forward(lib):
     layer.forward(X, ids, w)
     layer.backward(X)
     layer.backward(X)  # of the same forward pass once more
+
+
+def test_accumulate_and_keep8_are_truth_values(lib):
+    """Any truth value picks a plan."""
+    layer, (X, ids, w) = layer_of(), inputs()
+    layer.forward(X, ids, w, keep8=torch.tensor(1))
+    layer.backward(X, accumulate=2)
+    run = [a for n, a, _ in lib.calls if n == "gemm_grouped_run"]
+    dw1 = [a for a in run if a[6] is layer.dW1]
+    assert dw1[0][0].desc.has_c == 1 and dw1[0][5] is layer.dW1 and dw1[0][2] is layer.xcodes
