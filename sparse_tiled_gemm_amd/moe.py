@@ -7,12 +7,21 @@ include/gemm_moe.h: the path that runs them together.
 
 W1 (experts x 2F x H) holds each expert's gate and up projection, W2 (experts
 x H x F) its down projection; X is tokens x H, ids (int32 or int64) and
-weights (fp32) are tokens x topk, an id out of range drops its slot.  All buffers are made
-once; a step only enqueues kernels, so it may be captured into a HIP graph.
+weights (fp32) are tokens x topk, an id out of range drops its slot.  dW1 and
+dW2 (fp32) have W1's and W2's layout.
 
-Between the passes the layer keeps the input of the activation in 8 bits
-(half the bytes) and, with keep8, its sorted input rows too.  `python -m
-sparse_tiled_gemm_amd.moe` runs a step and prints the time of each part.
+All buffers are made once and belong to the layer, those it returns among
+them: Y is overwritten by the next forward(), the gradients by the next
+backward().  A step only enqueues kernels, so it may be captured into a HIP
+graph.
+
+backward() is the gradient of the last forward().  It reads the input of the
+activation as 8-bit codes and, after forward(keep8=True), the sorted input
+rows for dW1 as well: half the bytes, at 4 significant bits.  The 16-bit
+buffers those come from (GU, and Xs) are then free between the passes, but
+this layer keeps them, so that it takes no less memory for the codes.
+
+`python -m sparse_tiled_gemm_amd.moe` runs a step and prints the time of each part.
 """
 import torch
 
