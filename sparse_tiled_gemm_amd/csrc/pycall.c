@@ -4,8 +4,8 @@
  * data_ptr() method (a torch tensor).  The x86-64 calling convention passes
  * every such argument as one 64-bit word, of which a 32-bit parameter takes
  * the low half.  Against ctypes a call of twelve arguments, tensors among
- * them, takes 0.6 instead of 2.0 us, which counts where a call is all there is
- * (a decoder's few tokens). */
+ * them, takes 0.5 instead of 1.7 us (0.05 of it for letting other threads
+ * run), which counts where a call is all there is (a decoder's few tokens). */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
@@ -63,13 +63,17 @@ static PyObject *call(PyObject *self, PyObject *const *args, Py_ssize_t n)
     for (i = 1; i < n; ++i)
         if (word(args[i], &a[i - 1]))
             return NULL;
-    /* words past a function's parameters are not read by it */
+    /* A launch may wait (for room in a queue, for code to be loaded): other
+     * threads run meanwhile.  The caller holds references to the arguments.
+     * Words past a function's parameters are not read by it. */
+    Py_BEGIN_ALLOW_THREADS
     if (n <= 9)
         r = ((int (*)(W8))f)(A8(0));
     else if (n <= 13)
         r = ((int (*)(W8, W4))f)(A8(0), A4(8));
     else
         r = ((int (*)(W8, W8, W4))f)(A8(0), A8(8), A4(16));
+    Py_END_ALLOW_THREADS
     return PyLong_FromLong(r);
 }
 

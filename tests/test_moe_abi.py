@@ -212,3 +212,27 @@ def test_arguments_of_the_wrong_kind():
             _pycall.call(*bad)
     with pytest.raises(ValueError):
         _pycall.call(0, 1)
+
+
+def test_calls_let_other_threads_run():
+    """A call that waits (a full queue, a first launch) stops its own thread only."""
+    import threading
+    import time
+
+    from sparse_tiled_gemm_amd import _pycall
+    usleep = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+    begun, seen = threading.Event(), []
+
+    def other():
+        begun.wait()
+        for _ in range(4):
+            time.sleep(0.05)
+            seen.append(time.monotonic())
+
+    t = threading.Thread(target=other)
+    t.start()
+    begun.set()
+    assert _pycall.call(usleep, 900000) == 0
+    end = time.monotonic()
+    t.join()
+    assert seen[0] < end - 0.3
