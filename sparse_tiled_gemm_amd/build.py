@@ -80,10 +80,10 @@ def _stale(src):
 
 
 def build(verbose=False, asm=False, incremental=False):
-    """Compile every source and the binding's call (incremental=True: only those whose object is
-    older than the source or a header) and link libstgemm.so."""
+    """Compile every source (incremental=True: only those whose object is
+    older than the source or a header) and link libstgemm.so, then build the
+    binding's call, which needs a C compiler and Python's headers besides."""
     os.makedirs(BUILD, exist_ok=True)
-    _build_pycall(verbose)
     todo = [s for s in SOURCES if not incremental or asm or _stale(s)]
     if todo:
         with concurrent.futures.ThreadPoolExecutor(max_workers=len(todo)) as ex:
@@ -95,6 +95,7 @@ def build(verbose=False, asm=False, incremental=False):
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _build_pycall(verbose)
     return LIB
 
 
