@@ -344,3 +344,47 @@ def test_codes_past_32_bits(algo):
         ref, S = R.weights_ref(A, Bv, offsets)
         bound = R.half_step("f32", ref) * 1.001 + rows * 2 * R.U32 * S
         assert ((D[:, :, c:c + 192].cpu().double() - ref).abs() <= bound).all(), plan.name
+
+
+EIGHT = ["auto", "generic", "tiled64", "tiled128", "tiled256"]
+
+
+@pytest.mark.parametrize("algo", EIGHT)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_every_code_and_scale_of_an_8_bit_operand(dtype, algo):
+    """Each value enters as the one gemm_q8_load gives: groups of one row and
+    a single 1 in A leave it as it is."""
+    say("codes", dtype, algo)
+    codes = torch.arange(256, dtype=torch.uint8).repeat(256, 1)
+    scales = torch.arange(256, dtype=torch.uint8).view(256, 1).repeat(1, 8)
+    K = 8
+    A = torch.zeros(256, K, dtype=R.DT[dtype])
+    A[:, 0] = 1
+    plan = _plan(algo, "weights", 256, 256, K, 256, dtype, "e4m3", "f32")
+    D = torch.full((256, K, 256), 5.0, device="cuda")
+    off_d = torch.arange(257, dtype=torch.int32, device="cuda")
+    G.gemm_grouped_run(plan, A.cuda(), codes.cuda(), scales.cuda(), off_d, None, D)
+    torch.cuda.synchronize()
+    want = R.q8_load_ref(codes, scales, dtype).float()
+    got = D.cpu()[:, 0]
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(got[~nan], want[~nan]), plan.name
+
+
+@pytest.mark.parametrize("algo", EIGHT)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_every_code_in_every_row_of_a_tile(dtype, algo):
+    """The same for one group of all rows and an identity for A (no NaN codes,
+    which would reach every row)."""
+    say("codes by row", dtype, algo)
+    codes = torch.arange(256, dtype=torch.uint8).repeat(256, 1)
+    codes[codes & 0x7F == 0x7F] = 0
+    scales = torch.arange(256, dtype=torch.uint8).clamp(max=254).view(256, 1).repeat(1, 8)
+    plan = _plan(algo, "weights", 256, 256, 256, 1, dtype, "e4m3", "f32")
+    D = torch.full((256, 256), 5.0, device="cuda")
+    off_d = torch.tensor([0, 256], dtype=torch.int32, device="cuda")
+    G.gemm_grouped_run(plan, torch.eye(256, dtype=R.DT[dtype]).cuda(), codes.cuda(), scales.cuda(),
+                       off_d, None, D)
+    torch.cuda.synchronize()
+    assert torch.equal(D.cpu(), R.q8_load_ref(codes, scales, dtype).float()), plan.name
