@@ -4,6 +4,7 @@ another stream, and captured into a HIP graph."""
 import pytest
 import torch
 
+import moe_ref as R
 from gpu_util import say
 from sparse_tiled_gemm_amd import moe
 
@@ -185,3 +186,45 @@ def test_weights_changed_between_the_passes():
         for a, b in zip(out, want):
             assert torch.equal(a, b)
             a.fill_(5)
+
+
+def _from_codes(layer, X, dY, w, ids, W1, W2):
+    """dX, dW1 and dW2 in 64 bits from the values that the layer kept."""
+    v = R.q8_values(layer.codes.cpu(), layer.scales.cpu())
+    xv = R.q8_values(layer.xcodes.cpu(), layer.xscales.cpu()) if layer.keep8 else None
+    pos = layer.pos.cpu().view(ids.shape)
+    X, dY, w, W1, W2 = (t.double() for t in (X, dY, w, W1, W2))
+    inner = W2.shape[2]
+    dX, dW1, dW2 = torch.zeros_like(X), torch.zeros_like(W1), torch.zeros_like(W2)
+    for t in range(len(X)):
+        for k, e in enumerate(ids[t].tolist()):
+            if e < 0:
+                continue
+            p = int(pos[t, k])
+            dys = w[t, k] * dY[t]
+            (dg, du, h), _ = R.swiglu_backward_ref(v[p, :inner], v[p, inner:], W2[e].t() @ dys)
+            dgu = torch.cat([dg, du])
+            dW2[e] += torch.outer(dys, h)
+            dW1[e] += torch.outer(dgu, X[t] if xv is None else xv[p])
+            dX[t] += W1[e].t() @ dgu
+    return dX, dW1, dW2
+
+
+@pytest.mark.parametrize("keep8", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("tokens,hidden,inner,groups,topk,drop", [
+    (37, 64, 40, 5, 2, 0.1), (1, 128, 64, 8, 2, 0.0), (150, 72, 104, 3, 3, 0.3)])
+def test_gradients_at_the_kept_values(tokens, hidden, inner, groups, topk, drop, dtype, keep8):
+    """Against the gradient at the values the codes stand for, what is left
+    are the roundings of the 16-bit tensors on the way, half a step each: dYs,
+    dH, dGU, dXs, dX for dX; dYs, dH, dGU for dW1; dYs, H for dW2."""
+    say("kept values", tokens, hidden, inner, groups, topk, drop, dtype, keep8)
+    p = _problem(tokens, hidden, inner, groups, topk, dtype, tokens + 1, drop)
+    layer = moe.ExpertMLP(p[4].cuda(), p[5].cuda(), tokens, topk)
+    layer.forward(p[0].cuda(), p[3].cuda(), p[2].cuda(), keep8=keep8)
+    dX, _, dW1, dW2 = layer.backward(p[1].cuda())
+    torch.cuda.synchronize()
+    half = torch.finfo(dtype).eps / 2
+    for got, want, n, what in zip((dX, dW1, dW2), _from_codes(layer, *p), (5, 3, 2),
+                                  ("dX", "dW1", "dW2")):
+        _close(got, want, n * half, what)
