@@ -11,6 +11,11 @@ __device__ STG_AI inline float e8m0(uint32_t s)
     return __builtin_bit_cast(float, b);
 }
 
+// The largest scale byte under which every code's value lies in the type's
+// range: 448 * 2^(byte - 127).
+template <bool BF>
+constexpr uint32_t MAX_SCALE = BF ? 246 : 134;
+
 // x clamped to the finite range of the 16-bit type (NaN stays NaN).
 template <bool BF>
 __device__ STG_AI inline float clamp16(float x)
