@@ -376,11 +376,18 @@ static bool grouped_tiled_ok(const gemm_grouped_desc_t &d)
 static int choose_family(const gemm_grouped_desc_t &d, int num_cu)
 {
     if (d.mode == GEMM_GROUPED_WEIGHTS) {
-        // While 64 x 64 tiles fit the chip (three per compute unit at once) a
-        // tile's way through the rows is the time: 4 groups of 3400 rows, 704
-        // x 480, 34 with 64, 68 with 128; 2048 x 1024, 65 and 59.  The same
-        // for 128 against 256: 4 groups of 2048 rows, 2048 x 1024, 57 and 75;
-        // 3 of 1200, 5904 x 448, 67 and 85; 2048 x 4096, 199 and 144.
+        // With few tiles a tile's way through the rows is the time, which
+        // smaller tiles shorten: 4 groups of 3400 rows, 704 x 480, 34 with 64,
+        // 68 with 128; 2048 x 1024, 65 and 59.  Two workgroups of 64 x 64 tiles
+        // (64 KB of LDS) run on a compute unit at once, and yet the border is
+        // three tiles per compute unit: over drawn shapes (some 90 to each
+        // quarter, 16-bit / 8-bit B) 64's time over 128's is, as a geometric
+        // mean, 0.79 / 0.79 from 1.5 to 2 tiles per compute unit, 0.90 / 0.93,
+        // 0.97 / 0.95, 1.00 / 0.99, 0.99 / 1.01 in the quarters from 2 to 3, 1.02 /
+        // 1.05 from 3 to 3.5 and 1.06 / 1.17 from 4 to 6.  The same for 128
+        // against 256: 4 groups of 2048 rows, 2048 x 1024, 57 and 75; 3 of
+        // 1200, 5904 x 448, 67 and 85; 2048 x 4096, 199 and 144; drawn shapes 0.66 /
+        // 0.64 from 1.5 to 2, 0.77-0.83 / 0.71-0.77 from 2 to 3.
         const int64_t t64 = d.groups * ceil_div(d.K, 64) * ceil_div(d.N, 64);
         const int64_t t128 = d.groups * ceil_div(d.K, 128) * ceil_div(d.N, 128);
         const int64_t t256 = d.groups * ceil_div(d.K, 256) * ceil_div(d.N, 256);
