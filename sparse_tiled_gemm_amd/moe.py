@@ -8,7 +8,9 @@ include/gemm_moe.h: the path that runs them together.
 W1 (experts x 2F x H) holds each expert's gate and up projection, W2 (experts
 x H x F) its down projection; X is tokens x H, ids (int32 or int64) and
 weights (fp32) are tokens x topk, an id out of range drops its slot.  dW1 and
-dW2 (fp32) have W1's and W2's layout.
+dW2 (fp32) have W1's and W2's layout.  Each forward() uses W1 and W2 as they
+are then (contiguous ones are read where they lie, others copied first); they
+must not change before its backward().
 
 All buffers are made once and belong to the layer, those it returns among
 them: Y is overwritten by the next forward(), the gradients by the next
@@ -55,7 +57,10 @@ class ExpertMLP:
                 two_f % 2 or W1.dtype not in _NAME:
             raise ValueError("W1 (experts x 2F x H) and W2 (experts x H x F) in f16 or bf16")
         _check_device(W1.device, W1=W1, W2=W2)
-        self.W1, self.W2 = W1.contiguous(), W2.contiguous()
+        # weights that are not contiguous: copies, renewed by each forward pass
+        self.W1, self.W2 = (w if w.is_contiguous() else w.detach().contiguous() for w in (W1, W2))
+        self.copied = [(own, given) for own, given in ((self.W1, W1), (self.W2, W2))
+                       if own is not given]
         self.tokens, self.topk = tokens, topk
         dt, dev = W1.dtype, W1.device
         self.dtype = _NAME[dt]
@@ -98,6 +103,8 @@ class ExpertMLP:
         if ids.dtype not in (torch.int32, torch.int64):
             raise ValueError("ids in int32 or int64")
         _check_device(self.W1.device, X=X, ids=ids, weights=weights)
+        for own, given in self.copied:
+            own.copy_(given.detach())
         self.weights.copy_(weights.detach())  # no graph of the caller's
         X, ldx = _rows(X)
         G.gemm_moe_dispatch(T, K, self.groups, h, t, ids, X, ldx, self.offsets, self.order,

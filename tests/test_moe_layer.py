@@ -180,3 +180,26 @@ def test_accumulate_and_keep8_are_truth_values(lib):
     run = [a for n, a, _ in lib.calls if n == "gemm_grouped_run"]
     dw1 = [a for a in run if a[6] is layer.dW1]
     assert dw1[0][0].desc.has_c == 1 and dw1[0][5] is layer.dW1 and dw1[0][2] is layer.xcodes
+
+
+def test_weights_in_any_layout_follow_updates(lib):
+    """Weights changed in place between steps are the ones the next step
+    uses, contiguous or not."""
+    gen = torch.Generator().manual_seed(1)
+    w1 = torch.randn(E, H, 2 * F, generator=gen).bfloat16()
+    w2 = torch.randn(H, E, F, generator=gen).bfloat16()
+    for W1, W2 in [(w1.transpose(1, 2), w2.transpose(0, 1)),
+                   (w1.transpose(1, 2).contiguous(), w2.transpose(0, 1).contiguous())]:
+        layer = moe.ExpertMLP(dev(W1), dev(W2), T, K)
+        X, ids, w = inputs()
+        for _ in range(2):
+            lib.calls.clear()
+            layer.forward(X, ids, w)
+            layer.backward(X)
+            products = [a[2] for n, a, _ in lib.calls if n == "gemm_grouped_run"]
+            for got, want in [(products[0], W1), (products[1], W2), (products[2], W2),
+                              (products[5], W1)]:
+                assert torch.equal(got, want) and got.is_contiguous()
+            W1.mul_(-2)
+            W2.add_(1)
+    assert layer.W1.data_ptr() == W1.data_ptr()  # contiguous ones are read where they lie
