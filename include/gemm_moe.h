@@ -122,7 +122,11 @@ gemm_status_t gemm_moe_combine_backward(int64_t tokens, int64_t topk, int64_t co
  *
  * The fast kernels move 16-byte chunks: K, lda and ldb (and N where B is
  * row-major) in multiples of 8, leading dimensions below 2^21, A and B 16-byte
- * aligned; everything else runs a generic kernel.
+ * aligned.  Everything else runs a generic kernel, which takes some 30 (ROWS)
+ * or 10 (WEIGHTS) times as long on large products (4 groups of 512 rows, 2048 x
+ * 2048 bf16: 889 and 31 us, 297 and 28).  Alignment is known at the call only:
+ * a plan of any family runs the generic kernel for A or B off 16 bytes, and
+ * gemm_grouped_plan_describe names the kernel of aligned ones.
  *
  * a_type GEMM_F16 or GEMM_BF16; d_type GEMM_F32, GEMM_F16 or GEMM_BF16; fp32
  * accumulation, one rounding.  1 <= groups <= 65535; rows, N, K below 2^31;

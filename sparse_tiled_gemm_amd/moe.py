@@ -47,6 +47,8 @@ def _check_device(device, **tensors):
     for name, x in tensors.items():
         if not x.is_cuda or x.device != device:
             raise ValueError("%s has to lie on the weights' GPU" % name)
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        raise ValueError("the weights' GPU has to be the current one")
 
 
 class ExpertMLP:

@@ -203,3 +203,14 @@ def test_weights_in_any_layout_follow_updates(lib):
             W1.mul_(-2)
             W2.add_(1)
     assert layer.W1.data_ptr() == W1.data_ptr()  # contiguous ones are read where they lie
+
+
+def test_the_weights_gpu_is_the_current_one(monkeypatch):
+    """The library launches on the current device: addresses of another
+    device's memory do not go to it."""
+    x = types.SimpleNamespace(is_cuda=True, device=torch.device("cuda", 1))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError):
+        moe._check_device(x.device, X=x)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    moe._check_device(x.device, X=x)
