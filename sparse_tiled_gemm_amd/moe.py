@@ -15,7 +15,7 @@ must not change before its backward().
 All buffers are made once and belong to the layer, those it returns among
 them: Y is overwritten by the next forward(), the gradients by the next
 backward().  A step only enqueues kernels, so it may be captured into a HIP
-graph.
+graph (rows of X or dY that share memory are copied out first).
 
 backward() is the gradient of the last forward().  It reads the input of the
 activation as 8-bit codes and, after forward(keep8=True), the sorted input
