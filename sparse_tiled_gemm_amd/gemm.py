@@ -290,7 +290,10 @@ _at = _Addresses()
 
 def _call(address, *args):
     global _call
-    from . import _pycall
+    try:
+        from . import _pycall
+    except ImportError as e:
+        raise RuntimeError("_pycall.so is not built; run `python -m sparse_tiled_gemm_amd.build`") from e
     _call = _pycall.call  # from now on directly
     return _call(address, *args)
 

@@ -1,6 +1,7 @@
 """The C library is built whatever becomes of the Python binding's call."""
 import os
 import subprocess
+import sys
 
 import pytest
 
@@ -29,3 +30,16 @@ def test_the_library_needs_no_python_headers(monkeypatch, tmp_path):
         B.build()
     assert os.path.exists(B.LIB) and sorted(compiled) == sorted(B.SOURCES)
     assert not os.path.exists(B.PYCALL)
+
+
+def test_a_missing_extension_module_is_named():
+    """As a missing library: what to run."""
+    code = ("import sys; sys.modules['sparse_tiled_gemm_amd._pycall'] = None\n"
+            "from sparse_tiled_gemm_amd import gemm as G\n"
+            "try:\n"
+            "    G.gemm_q8_store(0, 0, 'bf16', None, 0, None, None, stream=0)\n"
+            "except RuntimeError as e:\n"
+            "    assert 'sparse_tiled_gemm_amd.build' in str(e), e\n"
+            "else:\n"
+            "    raise AssertionError\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=B.ROOT)
