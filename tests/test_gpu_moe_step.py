@@ -6,6 +6,7 @@ import torch
 
 import moe_ref as R
 from gpu_util import say
+from sparse_tiled_gemm_amd import gemm as G
 from sparse_tiled_gemm_amd import moe
 
 pytestmark = pytest.mark.gpu
@@ -228,3 +229,11 @@ def test_gradients_at_the_kept_values(tokens, hidden, inner, groups, topk, drop,
     for got, want, n, what in zip((dX, dW1, dW2), _from_codes(layer, *p), (5, 3, 2),
                                   ("dX", "dW1", "dW2")):
         _close(got, want, n * half, what)
+
+
+def test_the_current_stream_is_torch_s():
+    """The binding's look-up of the stream against torch's public one."""
+    for s in (torch.cuda.default_stream(), torch.cuda.Stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(s):
+            assert G._stream(None) == s.cuda_stream == torch.cuda.current_stream().cuda_stream
+            assert G._stream(s) == s.cuda_stream
