@@ -22,7 +22,8 @@ SOURCES = ["gemm_api.cpp", "kernels_dense.hip", "kernels_sparse.hip", "kernels_m
            "kernels_w4.hip", "kernels_mn.hip", "kernels_diag.hip", "kernels_k16.hip",
            "moe_api.cpp", "kernels_route.hip", "kernels_q8.hip", "kernels_grouped.hip",
            "kernels_grouped_rows.hip", "kernels_grouped_weights.hip",
-           "kernels_grouped_skinny.hip"]
+           "kernels_grouped_skinny.hip", "vocab_api.cpp", "kernels_embed.hip",
+           "kernels_xent.hip", "kernels_xent_logits.hip", "kernels_xent_grad.hip"]
 
 PYCALL = os.path.join(HERE, "_pycall.so")  # csrc/pycall.c, the binding's call
 

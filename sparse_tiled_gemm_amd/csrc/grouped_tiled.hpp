@@ -300,11 +300,12 @@ struct SmallShape {
 };
 
 // The operands of the tile of group t at (m_blk, n_blk); M, K: its group's
-// rows (of the output) and sum.
+// rows (of the output) and sum; KB: an MN-major B's K rows, if fewer exist.
 template <class S>
 __device__ STG_AI inline void set_operands(typename S::OpA &A, typename S::OpB &B,
                                            const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
-                                           int64_t n_blk, int64_t M, int64_t K, int lane, int wave)
+                                           int64_t n_blk, int64_t M, int64_t K, int64_t KB,
+                                           int lane, int wave)
 {
     A.ld = a.lda * 2;
     if constexpr (S::ALAY == GL_K) {
@@ -324,7 +325,7 @@ __device__ STG_AI inline void set_operands(typename S::OpA &A, typename S::OpB &
         B.span = a.N - n_blk;
     } else {
         B.base = (const uint8_t *)a.B + (S::W ? t.r0 : (int64_t)t.g * a.K) * B.ld + n_blk * BE;
-        B.k_bytes = K;
+        B.k_bytes = KB;
         B.span = (a.N - n_blk) * BE;
     }
     if constexpr (S::BLAY == GL_Q8) {
@@ -350,19 +351,17 @@ __device__ STG_AI inline void tile_barrier()
 }
 
 // A wave's accumulators to the output, through 32-row slabs in `lds`; in as
-// many pieces as its rows and columns lie in.
+// many pieces as its rows and columns lie in.  whole_lines: D's rows start on
+// cache lines.
 template <class OP, class S>
-__device__ STG_AI inline void store_tile(const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
-                                         int64_t n_blk, int64_t M,
-                                         typename OP::acc_t (&acc)[S::FM][S::FN], int lane,
-                                         int wave, uint32_t *lds)
+__device__ STG_AI inline void store_acc(const EpiArgs &e, int whole_lines, int64_t m_blk,
+                                        int64_t n_blk, typename OP::acc_t (&acc)[S::FM][S::FN],
+                                        int lane, int wave, uint32_t *lds)
 {
     typedef typename S::OpA OpA;
     typedef typename S::OpB OpB;
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
-    EpiArgs e = group_epilogue(a, t.g, t.r0, M);
-    e.vec = a.vec;
     constexpr int PA = S::PA, PB = S::PB;
     auto store = [&](auto p, auto q, auto cpol) STG_AI {
         constexpr int C = decltype(cpol)::value;
@@ -376,9 +375,9 @@ __device__ STG_AI inline void store_tile(const GroupedArgs &a, const GroupRows &
 #pragma unroll
             for (int j = 0; j < FN; ++j)
                 part[i][j] = acc[I + i][J + j];
-        if (a.d_kind == OUT_F32)
+        if (e.d_kind == OUT_F32)
             epilogue_slabs<OP, FM, FN, OUT_F32, C>(e, part, m0, n0, lane, lds);
-        else if (a.d_kind == OUT_F16)
+        else if (e.d_kind == OUT_F16)
             epilogue_slabs<OP, FM, FN, OUT_F16, C>(e, part, m0, n0, lane, lds);
         else
             epilogue_slabs<OP, FM, FN, OUT_BF16, C>(e, part, m0, n0, lane, lds);
@@ -396,18 +395,48 @@ __device__ STG_AI inline void store_tile(const GroupedArgs &a, const GroupRows &
     // want them), parts of lines have to meet there: with rows of 60.25 lines
     // non-temporal stores took 163 us, plain ones 67 (12 groups of 2944 x
     // 1928).
-    if (a.whole_lines)
+    if (whole_lines)
         pieces(std::integral_constant<int, EPI_CPOL>{});
     else
         pieces(std::integral_constant<int, 0>{});
 }
 
-// One BM x BN tile of group t at (m_blk, n_blk); M, K: its group's rows (of
-// the output) and sum.
+// The accumulators of group t's tile at (m_blk, n_blk); M: the group's rows
+// (of the output).
+template <class OP, class S>
+__device__ STG_AI inline void store_tile(const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
+                                         int64_t n_blk, int64_t M,
+                                         typename OP::acc_t (&acc)[S::FM][S::FN], int lane,
+                                         int wave, uint32_t *lds)
+{
+    EpiArgs e = group_epilogue(a, t.g, t.r0, M);
+    e.vec = a.vec;
+    store_acc<OP, S>(e, a.whole_lines, m_blk, n_blk, acc, lane, wave, lds);
+}
+
+// The LDS of wave `wave` after the K loop: a slab of 32 rows lies in the
+// region of its number.
+__device__ STG_AI inline uint32_t *wave_slab(const Regions &L, int wave)
+{
+    uint8_t *slab = wave == 0   ? L.a00
+                    : wave == 1 ? L.a10
+                    : wave == 2 ? L.a01
+                    : wave == 3 ? L.a11
+                    : wave == 4 ? L.b00
+                    : wave == 5 ? L.b10
+                    : wave == 6 ? L.b01
+                                : L.b11;
+    return (uint32_t *)slab;
+}
+
+// The sums of one BM x BN tile of group t at (m_blk, n_blk); M, K: its group's
+// rows (of the output) and sum; KB: see set_operands.  LDS is free afterwards.
 template <class OP, bool W, int ALAY, int BLAY, int BM, int BN>
-__device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
-                                        int64_t n_blk, int64_t M, int64_t K, int lane, int wave,
-                                        const Regions &L)
+__device__ STG_AI inline void
+tile_sum(const GroupedArgs &a, const GroupRows &t, int64_t m_blk, int64_t n_blk, int64_t M, int64_t K,
+         int64_t KB, int lane, int wave, const Regions &L,
+         typename OP::acc_t (&acc)[TileShape<OP, W, ALAY, BLAY, BM, BN>::FM]
+                                  [TileShape<OP, W, ALAY, BLAY, BM, BN>::FN])
 {
     typedef TileShape<OP, W, ALAY, BLAY, BM, BN> S;
     constexpr int FA = S::FA, FB = S::FB;
@@ -429,9 +458,8 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
     using I1 = std::integral_constant<int, 1>;
     OpA A;
     OpB B;
-    set_operands<S>(A, B, a, t, m_blk, n_blk, M, K, lane, wave);
+    set_operands<S>(A, B, a, t, m_blk, n_blk, M, K, KB, lane, wave);
 
-    typename OP::acc_t acc[2 * FA][2 * FB];
 #pragma unroll
     for (int i = 0; i < 2 * FA; ++i)
 #pragma unroll
@@ -550,17 +578,18 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
         STG_WAIT_VMCNT(0); // copies past the last tile, before LDS is reused
         tile_barrier();
     }
+}
 
-    // a wave's slab of 32 rows lies in the region of its number
-    uint8_t *slab = wave == 0   ? L.a00
-                    : wave == 1 ? L.a10
-                    : wave == 2 ? L.a01
-                    : wave == 3 ? L.a11
-                    : wave == 4 ? L.b00
-                    : wave == 5 ? L.b10
-                    : wave == 6 ? L.b01
-                                : L.b11;
-    store_tile<OP, S>(a, t, m_blk, n_blk, M, acc, lane, wave, (uint32_t *)slab);
+// The tile's sums, stored.
+template <class OP, bool W, int ALAY, int BLAY, int BM, int BN>
+__device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
+                                        int64_t n_blk, int64_t M, int64_t K, int lane, int wave,
+                                        const Regions &L)
+{
+    typedef TileShape<OP, W, ALAY, BLAY, BM, BN> S;
+    typename OP::acc_t acc[S::FM][S::FN];
+    tile_sum<OP, W, ALAY, BLAY, BM, BN>(a, t, m_blk, n_blk, M, K, K, lane, wave, L, acc);
+    store_tile<OP, S>(a, t, m_blk, n_blk, M, acc, lane, wave, wave_slab(L, wave));
 }
 
 // A 64 x 64 tile, for products of few tiles: there the time is a workgroup's
@@ -572,16 +601,21 @@ __device__ STG_AI inline void tile_body(const GroupedArgs &a, const GroupRows &t
 // the copies of t + 3 go where t - 1 was.  An 8-bit B of tile t + 1 (loaded two
 // tiles before) is stored after the reads of t.
 template <class OP, bool W, int ALAY, int BLAY>
-__device__ STG_AI inline void small_body(const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
-                                         int64_t n_blk, int64_t M, int64_t K, int lane, int wave,
-                                         uint8_t *s0, uint8_t *s1, uint8_t *s2, uint8_t *s3)
+__device__ STG_AI inline void small_sum(const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
+                                        int64_t n_blk, int64_t M, int64_t K, int64_t KB, int lane,
+                                        int wave, uint8_t *s0, uint8_t *s1, uint8_t *s2,
+                                        uint8_t *s3, typename OP::acc_t (&acc)[2][2])
 {
     typedef SmallShape<OP, W, ALAY, BLAY> S;
     constexpr int RB = 64 * 128; // bytes of a region: A, B in a buffer
     typename S::OpA A;
     typename S::OpB B;
-    set_operands<S>(A, B, a, t, m_blk, n_blk, M, K, lane, wave);
-    typename OP::acc_t acc[2][2] = {};
+    set_operands<S>(A, B, a, t, m_blk, n_blk, M, K, KB, lane, wave);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            acc[i][j] = typename OP::acc_t{};
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
@@ -650,6 +684,16 @@ __device__ STG_AI inline void small_body(const GroupedArgs &a, const GroupRows &
         STG_WAIT_VMCNT(0); // copies past the last tile, before LDS is reused
         tile_barrier();
     }
+}
+
+template <class OP, bool W, int ALAY, int BLAY>
+__device__ STG_AI inline void small_body(const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
+                                         int64_t n_blk, int64_t M, int64_t K, int lane, int wave,
+                                         uint8_t *s0, uint8_t *s1, uint8_t *s2, uint8_t *s3)
+{
+    typedef SmallShape<OP, W, ALAY, BLAY> S;
+    typename OP::acc_t acc[2][2];
+    small_sum<OP, W, ALAY, BLAY>(a, t, m_blk, n_blk, M, K, K, lane, wave, s0, s1, s2, s3, acc);
     uint8_t *slab = wave == 0 ? s0 : wave == 1 ? s1 : wave == 2 ? s2 : s3;
     store_tile<OP, S>(a, t, m_blk, n_blk, M, acc, lane, wave, (uint32_t *)slab);
 }

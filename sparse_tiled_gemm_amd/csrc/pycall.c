@@ -3,7 +3,9 @@
  * gemm_status_t.  An argument is an integer, None (NULL) or an object with a
  * data_ptr() method (a torch tensor).  The x86-64 calling convention passes
  * every such argument as one 64-bit word, of which a 32-bit parameter takes
- * the low half.  Against ctypes a call of twelve arguments, tensors among
+ * the low half.  call_float(address, args...) is for functions that take one
+ * float as well, given as a Python float: it goes into a register of its own,
+ * wherever it stands among the others.  Against ctypes a call of twelve arguments, tensors among
  * them, takes 0.5 instead of 1.7 us (0.05 of it for letting other threads
  * run), which counts where a call is all there is (a decoder's few tokens). */
 #define PY_SSIZE_T_CLEAN
@@ -44,13 +46,13 @@ static int word(PyObject *o, uint64_t *out)
 #define A4(i) a[i], a[i + 1], a[i + 2], a[i + 3]
 #define A8(i) A4(i), A4(i + 4)
 
-static PyObject *call(PyObject *self, PyObject *const *args, Py_ssize_t n)
+static PyObject *make_call(PyObject *const *args, Py_ssize_t n, int want_floats)
 {
     uint64_t a[20] = {0};
+    float x = 0.0f;
     uintptr_t f;
-    int r;
+    int r, words = 0, floats = 0;
     Py_ssize_t i;
-    (void)self;
     if (n < 1 || n > 21 || !PyLong_Check(args[0])) {
         PyErr_SetString(PyExc_TypeError, "call(address, up to 20 arguments)");
         return NULL;
@@ -60,25 +62,49 @@ static PyObject *call(PyObject *self, PyObject *const *args, Py_ssize_t n)
         PyErr_SetString(PyExc_ValueError, "address is NULL");
         return NULL;
     }
-    for (i = 1; i < n; ++i)
-        if (word(args[i], &a[i - 1]))
+    for (i = 1; i < n; ++i) {
+        if (want_floats && PyFloat_Check(args[i])) {
+            x = (float)PyFloat_AS_DOUBLE(args[i]);
+            ++floats;
+        } else if (word(args[i], &a[words++])) {
             return NULL;
+        }
+    }
+    if (floats != want_floats) {
+        PyErr_SetString(PyExc_TypeError, "exactly one float argument");
+        return NULL;
+    }
     /* A launch may wait (for room in a queue, for code to be loaded): other
      * threads run meanwhile.  The caller holds references to the arguments.
-     * Words past a function's parameters are not read by it. */
+     * Words past a function's parameters, and a float it has none for, are not
+     * read by it. */
     Py_BEGIN_ALLOW_THREADS
-    if (n <= 9)
-        r = ((int (*)(W8))f)(A8(0));
-    else if (n <= 13)
-        r = ((int (*)(W8, W4))f)(A8(0), A4(8));
+    if (words <= 8)
+        r = ((int (*)(W8, float))f)(A8(0), x);
+    else if (words <= 12)
+        r = ((int (*)(W8, W4, float))f)(A8(0), A4(8), x);
     else
-        r = ((int (*)(W8, W8, W4))f)(A8(0), A8(8), A4(16));
+        r = ((int (*)(W8, W8, W4, float))f)(A8(0), A8(8), A4(16), x);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(r);
 }
 
+static PyObject *call(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    return make_call(args, n, 0);
+}
+
+static PyObject *call_float(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    return make_call(args, n, 1);
+}
+
 static PyMethodDef methods[] = {
     {"call", (PyCFunction)(void (*)(void))call, METH_FASTCALL, "call(address, args...) -> status"},
+    {"call_float", (PyCFunction)(void (*)(void))call_float, METH_FASTCALL,
+     "call_float(address, args...) -> status, one of the arguments being a float"},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycall", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};

@@ -1,0 +1,517 @@
+// C ABI of the operators over a vocabulary: argument checks, plan choice,
+// workspace layout and launches.  The operations are documented in
+// include/gemm_vocab.h.
+#include <hip/hip_runtime.h>
+
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <new>
+
+#include "api_checks.hpp"
+#include "gemm_vocab.h"
+#include "vocab_args.hpp"
+
+using namespace stg;
+
+struct gemm_xent_plan {
+    gemm_xent_desc_t d; // normalised: packed leading dimensions filled in
+    int64_t hp;         // hidden in whole 16-byte chunks
+    int copy;           // W goes through the workspace
+    int stats, g, dx, dw; // XentTile of each product
+    int64_t piece;      // columns of a piece
+    int64_t dx_splits;  // parts of a piece whose sums dX's product keeps apart
+    int device;
+    char name[96];
+};
+
+namespace {
+
+bool is_float(int t) { return t == GEMM_F32 || is_16bit(t); }
+int64_t float_bytes(int t) { return t == GEMM_F32 ? 4 : 2; }
+int out_kind(int t) { return t == GEMM_F32 ? OUT_F32 : t == GEMM_F16 ? OUT_F16 : OUT_BF16; }
+
+// ---------------------------------------------------------------- embedding
+
+gemm_status_t check_embed(int64_t tokens, int64_t vocab, int64_t cols)
+{
+    if (tokens < 0 || vocab < 0 || cols < 0)
+        return fail(GEMM_ERR_INVALID_VALUE, "negative size");
+    if (tokens > (1 << 26) || vocab > EMBED_MAX_VOCAB || cols > (1 << 23))
+        return fail(GEMM_ERR_UNSUPPORTED, "at most 2^26 tokens, 2^20 rows and 2^23 columns");
+    return GEMM_OK;
+}
+
+gemm_status_t check_embed_types(int32_t e_type, int32_t y_type, int32_t id_bytes)
+{
+    for (int32_t t : {e_type, y_type}) {
+        if (t < GEMM_F16 || t > GEMM_U8)
+            return fail(GEMM_ERR_INVALID_VALUE, "unknown dtype code");
+        if (!is_float(t))
+            return fail(GEMM_ERR_UNSUPPORTED, "types must be f32, f16 or bf16");
+    }
+    if (id_bytes != 4 && id_bytes != 8)
+        return fail(GEMM_ERR_INVALID_VALUE, "id_bytes must be 4 or 8");
+    return GEMM_OK;
+}
+
+// Hands out 256-byte aligned parts of a workspace, or counts their bytes.
+struct Parts {
+    uint8_t *base;
+    size_t at = 0;
+    template <class T>
+    void take(T *&p, int64_t n)
+    {
+        p = base ? (T *)(base + at) : nullptr;
+        at += ((size_t)n * sizeof(T) + 255) / 256 * 256;
+    }
+};
+
+// The sort's sizes and the workspace of the gradient.
+size_t embed_parts(EmbedArgs &a, void *workspace)
+{
+    if (a.tokens <= EMBED_SMALL)
+        return 0;
+    int bits = 1;
+    while (((int64_t)1 << bits) < a.vocab)
+        ++bits;
+    a.hi_bits = bits / 2;
+    a.lo_bits = bits - a.hi_bits;
+    const int64_t c = ceil_div(a.tokens, 256);
+    a.chunk = (int)(c <= 1024 ? 1024 : ceil_div(c, 512) * 512); // eight waves, 64 at a time
+    a.chunks = (int)ceil_div(a.tokens, a.chunk);
+    Parts p{(uint8_t *)workspace};
+    p.take(a.counts, (int64_t)a.chunks << a.lo_bits);
+    p.take(a.bounds, ((int64_t)1 << a.lo_bits) + 1);
+    p.take(a.binned, a.tokens);
+    p.take(a.order, a.tokens);
+    p.take(a.key, a.tokens);
+    p.take(a.part, ceil_div(a.tokens, EMBED_RUN) * 2 * a.cols);
+    return p.at;
+}
+
+} // namespace
+
+extern "C" {
+
+gemm_status_t gemm_embed(int64_t tokens, int64_t vocab, int64_t cols, int32_t e_type,
+                         int32_t y_type, int32_t id_bytes, const void *ids, const void *E,
+                         int64_t lde, void *Y, int64_t ldy, float scale, gemm_stream_t stream)
+{
+    CHECK(check_embed(tokens, vocab, cols));
+    CHECK(check_embed_types(e_type, y_type, id_bytes));
+    CHECK(check_matrix("E", vocab, cols, &lde));
+    CHECK(check_matrix("Y", tokens, cols, &ldy));
+    CHECK(check_buffers({{"ids", ids, tokens, 1, 1, id_bytes, false},
+                         {"E", E, vocab, cols, lde, float_bytes(e_type), false},
+                         {"Y", Y, tokens, cols, ldy, float_bytes(y_type), true}}));
+    if (tokens == 0 || cols == 0)
+        return ok();
+    CHECK(check_gfx950());
+    EmbedArgs a{};
+    a.tokens = tokens;
+    a.vocab = vocab;
+    a.cols = cols;
+    a.id8 = id_bytes == 8;
+    a.ids = ids;
+    a.e_kind = out_kind(e_type);
+    a.y_kind = out_kind(y_type);
+    a.in = E;
+    a.ld_in = lde;
+    a.out = Y;
+    a.ld_out = ldy;
+    a.scale = scale;
+    return launched(launch_embed(a, (hipStream_t)stream));
+}
+
+gemm_status_t gemm_embed_workspace(int64_t tokens, int64_t vocab, int64_t cols, size_t *bytes)
+{
+    if (!bytes)
+        return fail(GEMM_ERR_NULL_POINTER, "bytes is NULL");
+    CHECK(check_embed(tokens, vocab, cols));
+    EmbedArgs a{};
+    a.tokens = tokens;
+    a.vocab = vocab;
+    a.cols = cols;
+    *bytes = embed_parts(a, nullptr);
+    return ok();
+}
+
+gemm_status_t gemm_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, int32_t y_type,
+                                  int32_t e_type, int32_t id_bytes, const void *ids,
+                                  const void *dY, int64_t lddy, void *dE, int64_t ldde,
+                                  int32_t accumulate, void *workspace, float scale,
+                                  gemm_stream_t stream)
+{
+    CHECK(check_embed(tokens, vocab, cols));
+    CHECK(check_embed_types(e_type, y_type, id_bytes));
+    if (accumulate != 0 && accumulate != 1)
+        return fail(GEMM_ERR_INVALID_VALUE, "accumulate must be 0 or 1");
+    CHECK(check_matrix("dY", tokens, cols, &lddy));
+    CHECK(check_matrix("dE", vocab, cols, &ldde));
+    EmbedArgs a{};
+    a.tokens = tokens;
+    a.vocab = vocab;
+    a.cols = cols;
+    const int64_t bytes = (int64_t)embed_parts(a, workspace);
+    CHECK(check_buffers({{"ids", ids, tokens, 1, 1, id_bytes, false},
+                         {"dY", dY, tokens, cols, lddy, float_bytes(y_type), false},
+                         {"dE", dE, vocab, cols, ldde, float_bytes(e_type), true},
+                         {"workspace", workspace, bytes, 1, 1, 1, true, 16}}));
+    if (vocab == 0 || cols == 0 || (tokens == 0 && accumulate))
+        return ok();
+    CHECK(check_gfx950());
+    a.id8 = id_bytes == 8;
+    a.ids = ids;
+    a.e_kind = out_kind(e_type);
+    a.y_kind = out_kind(y_type);
+    a.in = dY;
+    a.ld_in = lddy;
+    a.out = dE;
+    a.ld_out = ldde;
+    a.scale = scale;
+    a.accumulate = accumulate;
+    return launched(launch_embed_backward(a, (hipStream_t)stream));
+}
+
+// ---------------------------------------------------------------- linear cross entropy
+
+static bool normalise(gemm_xent_desc_t &d)
+{
+    auto fix = [&](int64_t &ld) {
+        if (ld == 0)
+            ld = d.hidden;
+        return ld >= d.hidden;
+    };
+    const bool x = fix(d.ldx), w = fix(d.ldw), dx = fix(d.lddx), dw = fix(d.lddw);
+    return x && w && dx && dw;
+}
+
+gemm_status_t gemm_xent_validate_desc(const gemm_xent_desc_t *desc)
+{
+    if (!desc)
+        return fail(GEMM_ERR_NULL_POINTER, "desc is NULL");
+    gemm_xent_desc_t d = *desc;
+    if (d.tokens < 0 || d.vocab < 1 || d.hidden < 1)
+        return fail(GEMM_ERR_INVALID_VALUE, "tokens must be >= 0, vocab and hidden >= 1");
+    auto dtype_ok = [](int t) { return t >= GEMM_F16 && t <= GEMM_U8; };
+    if (!dtype_ok(d.x_type) || !dtype_ok(d.dx_type) || !dtype_ok(d.dw_type))
+        return fail(GEMM_ERR_INVALID_VALUE, "unknown dtype code");
+    if (d.id_bytes != 4 && d.id_bytes != 8)
+        return fail(GEMM_ERR_INVALID_VALUE, "id_bytes must be 4 or 8");
+    if ((d.accumulate != 0 && d.accumulate != 1) || (d.unaligned != 0 && d.unaligned != 1))
+        return fail(GEMM_ERR_INVALID_VALUE, "accumulate and unaligned must be 0 or 1");
+    if (d.ldx < 0 || d.ldw < 0 || d.lddx < 0 || d.lddw < 0 || d.piece < 0)
+        return fail(GEMM_ERR_INVALID_VALUE, "negative leading dimension or piece");
+    if (!normalise(d))
+        return fail(GEMM_ERR_INVALID_VALUE, "leading dimension smaller than the matrix extent");
+    for (int64_t ld : {d.ldx, d.ldw, d.lddx, d.lddw})
+        if (ld > MAX_ELEMS || smul(d.tokens > d.vocab ? d.tokens : d.vocab, ld) > MAX_ELEMS)
+            return fail(GEMM_ERR_INVALID_VALUE, "a matrix spans more than 2^40 elements");
+    if (d.tokens > (1 << 24) || d.vocab > (1 << 24) || d.hidden > (1 << 20))
+        return fail(GEMM_ERR_UNSUPPORTED, "at most 2^24 tokens, 2^24 columns and 2^20 hidden values");
+    if (!is_16bit(d.x_type))
+        return fail(GEMM_ERR_UNSUPPORTED, "X must be f16 or bf16");
+    if (!is_float(d.dx_type) || !is_float(d.dw_type))
+        return fail(GEMM_ERR_UNSUPPORTED, "dX and dW must be f32, f16 or bf16");
+    // (2^31 threads in 256 x 256 tiles)
+    if (smul(ceil_div(d.tokens, 256), ceil_div(d.vocab, 256)) > (1 << 20))
+        return fail(GEMM_ERR_UNSUPPORTED, "more logits than one launch holds");
+    return ok();
+}
+
+static int64_t tiles(int t, int64_t m, int64_t n)
+{
+    return ceil_div(m, xent_edge(t)) * ceil_div(n, xent_edge(t));
+}
+
+// Tile of the logits' product of `n` columns.
+static int choose_logits(int64_t tokens, int64_t n, int num_cu)
+{
+    if (tokens <= 64)
+        return XT_64;
+    if (tokens <= 128 || tiles(XT_256, tokens, n) < num_cu)
+        return tiles(XT_128, tokens, n) < num_cu ? XT_64 : XT_128;
+    return XT_256;
+}
+
+static int choose_dw(int64_t piece, int64_t hp, int num_cu)
+{
+    if (tiles(XT_256, piece, hp) >= num_cu)
+        return XT_256;
+    return tiles(XT_128, piece, hp) >= num_cu ? XT_128 : XT_64;
+}
+
+static int choose_dx(int64_t tokens, int64_t hp)
+{
+    return tokens <= 64 || hp <= 64 ? XT_64 : tokens <= 128 || hp <= 128 ? XT_128 : XT_256;
+}
+
+static void choose(gemm_xent_plan_t &p, int num_cu)
+{
+    const gemm_xent_desc_t &d = p.d;
+    p.hp = ceil_div(d.hidden, 8) * 8;
+    // the main loop addresses 256 rows of W with 32-bit offsets
+    p.copy = d.hidden % 8 != 0 || d.ldw % 8 != 0 || d.ldw >= (1 << 21) || d.unaligned;
+    // G of a piece: 512 MB, W's copy too
+    int64_t most = ((int64_t)1 << 28) / (d.tokens > 0 ? d.tokens : 1);
+    if (p.copy && most > ((int64_t)1 << 28) / p.hp)
+        most = ((int64_t)1 << 28) / p.hp;
+    if (most > (1 << 20))
+        most = 1 << 20;
+    most = most < 2048 ? 2048 : most / 256 * 256;
+    if (d.piece > 0)
+        most = d.piece > (1 << 20) ? 1 << 20 : ceil_div(d.piece, 256) * 256;
+    const int64_t n = ceil_div(d.vocab, most);
+    p.piece = ceil_div(ceil_div(d.vocab, n), 256) * 256;
+    const int64_t cols = d.vocab < p.piece ? d.vocab : p.piece;
+    p.stats = choose_logits(d.tokens, p.copy ? cols : d.vocab, num_cu);
+    p.g = choose_logits(d.tokens, cols, num_cu);
+    p.dw = choose_dw(cols, p.hp, num_cu);
+    p.dx = choose_dx(d.tokens, p.hp);
+    if (const char *force = getenv("STGEMM_FORCE_KERNEL")) {
+        static const char *const names[XT_COUNT] = {"tiled64", "tiled128", "tiled256"};
+        for (int t = 0; t < XT_COUNT; ++t)
+            if (strcmp(force, names[t]) == 0)
+                p.stats = p.g = p.dw = p.dx = t;
+    }
+    // dX's sums run over the piece's columns: cut where its tiles would leave
+    // compute units idle, 1024 columns at least
+    const int64_t t = tiles(p.dx, d.tokens > 0 ? d.tokens : 1, p.hp);
+    int64_t s = t >= num_cu ? 1 : num_cu / t;
+    if (s > ceil_div(cols, 1024))
+        s = ceil_div(cols, 1024);
+    p.dx_splits = s < 1 ? 1 : s;
+}
+
+// The workspace of a call: args' pointers into it, its bytes.
+static size_t xent_parts(const gemm_xent_plan_t &p, bool backward, void *workspace, XentArgs &a,
+                         XentPiece &piece, float *&acc, uint16_t *&copy)
+{
+    const gemm_xent_desc_t &d = p.d;
+    Parts w{(uint8_t *)workspace};
+    w.take(a.count, 1);
+    w.take(a.pos, d.tokens);
+    w.take(a.map, d.tokens);
+    w.take(a.tgt, d.tokens);
+    w.take(a.Xc, d.tokens * p.hp);
+    if (backward) {
+        w.take(a.ca, d.tokens);
+        w.take(a.cb, d.tokens);
+        w.take(a.cl, d.tokens);
+        a.gmaxes = d.tokens > 0 ? ceil_div(d.tokens, XENT_PREP) : 1;
+        w.take(a.gmax, a.gmaxes);
+        w.take(acc, p.dx_splits * d.tokens * p.hp);
+        w.take(piece.G, d.tokens * p.piece);
+        piece.ldg = p.piece;
+    } else {
+        const int64_t e = xent_edge(p.stats), full = d.vocab / p.piece;
+        a.part_tiles = p.copy ? full * ceil_div(p.piece, e) + ceil_div(d.vocab - full * p.piece, e)
+                              : ceil_div(d.vocab, e);
+        w.take(a.zt, d.tokens);
+        w.take(a.part, a.part_tiles * d.tokens * 2);
+    }
+    if (p.copy)
+        w.take(copy, (d.vocab < p.piece ? d.vocab : p.piece) * p.hp);
+    return w.at;
+}
+
+gemm_status_t gemm_xent_plan(const gemm_xent_desc_t *desc, gemm_xent_plan_t **out)
+{
+    if (!out)
+        return fail(GEMM_ERR_NULL_POINTER, "out is NULL");
+    *out = nullptr;
+    CHECK(gemm_xent_validate_desc(desc));
+    int dev = 0;
+    DeviceInfo di;
+    CHECK(check_device(&dev, &di));
+    gemm_xent_plan_t *p = new (std::nothrow) gemm_xent_plan_t();
+    if (!p)
+        return fail(GEMM_ERR_INVALID_VALUE, "out of host memory");
+    p->d = *desc;
+    normalise(p->d);
+    p->device = dev;
+    choose(*p, di.num_cu);
+    snprintf(p->name, sizeof p->name, "xent_%s_stats%d_g%d_dx%dx%lld_dw%d%s",
+             p->d.x_type == GEMM_BF16 ? "bf16" : "f16", xent_edge(p->stats), xent_edge(p->g),
+             xent_edge(p->dx), (long long)p->dx_splits, xent_edge(p->dw), p->copy ? "_copy" : "");
+    static const bool log = [] {
+        const char *v = getenv("GEMM_LOG");
+        return v && *v && strcmp(v, "0") != 0;
+    }();
+    if (log)
+        fprintf(stderr, "[stgemm] xent plan tokens=%lld vocab=%lld hidden=%lld piece=%lld -> %s\n",
+                (long long)p->d.tokens, (long long)p->d.vocab, (long long)p->d.hidden,
+                (long long)p->piece, p->name);
+    *out = p;
+    return ok();
+}
+
+gemm_status_t gemm_xent_plan_destroy(gemm_xent_plan_t *plan)
+{
+    delete plan;
+    return ok();
+}
+
+gemm_status_t gemm_xent_plan_describe(const gemm_xent_plan_t *plan, char *buf, size_t len)
+{
+    if (!plan || !buf)
+        return fail(GEMM_ERR_NULL_POINTER, "plan or buf is NULL");
+    if (len == 0)
+        return fail(GEMM_ERR_INVALID_VALUE, "len is 0");
+    snprintf(buf, len, "%s", plan->name);
+    return ok();
+}
+
+gemm_status_t gemm_xent_workspace(const gemm_xent_plan_t *plan, size_t *forward, size_t *backward)
+{
+    if (!plan)
+        return fail(GEMM_ERR_NULL_POINTER, "plan is NULL");
+    XentArgs a{};
+    XentPiece p{};
+    float *acc;
+    uint16_t *copy;
+    if (forward)
+        *forward = xent_parts(*plan, false, nullptr, a, p, acc, copy);
+    if (backward)
+        *backward = xent_parts(*plan, true, nullptr, a, p, acc, copy);
+    return ok();
+}
+
+static void fill_args(XentArgs &a, const gemm_xent_plan_t &p, const void *X, const void *targets)
+{
+    a.tokens = p.d.tokens;
+    a.vocab = p.d.vocab;
+    a.hidden = p.d.hidden;
+    a.hp = p.hp;
+    a.id8 = p.d.id_bytes == 8;
+    a.bf16 = p.d.x_type == GEMM_BF16;
+    a.X = X;
+    a.ldx = p.d.ldx;
+    a.targets = targets;
+    a.scale = p.d.scale;
+}
+
+// A call's device, and W's alignment.
+static gemm_status_t check_call(const gemm_xent_plan_t &p, const void *W)
+{
+    int dev = 0;
+    CHECK(check_device(&dev, nullptr));
+    if (dev != p.device)
+        return fail(GEMM_ERR_DEVICE, "the plan was made on device %d, the current one is %d", p.device,
+                    dev);
+    if (!p.copy && !aligned(W, 16))
+        return fail(GEMM_ERR_MISALIGNED, "W is not aligned to 16 bytes and the plan has unaligned = 0");
+    return GEMM_OK;
+}
+
+// W's rows of a piece: where they lie, or copied.
+static hipError_t take_w(const gemm_xent_plan_t &p, const void *W, uint16_t *copy, XentPiece &piece,
+                         hipStream_t s)
+{
+    const uint16_t *w = (const uint16_t *)W + piece.v0 * p.d.ldw;
+    piece.W = p.copy ? copy : w;
+    piece.ldw = p.copy ? p.hp : p.d.ldw;
+    return p.copy ? launch_xent_copy({w, p.d.ldw, piece.n, p.d.hidden, p.hp, copy}, s) : hipSuccess;
+}
+
+#define LAUNCH(x)                                 \
+    do {                                          \
+        const hipError_t e_ = x;                  \
+        if (e_ != hipSuccess)                     \
+            return hip_fail(e_, "kernel launch"); \
+    } while (0)
+
+gemm_status_t gemm_xent_forward(const gemm_xent_plan_t *plan, const void *X, const void *W,
+                                const void *targets, float *loss, float *lse, void *workspace,
+                                gemm_stream_t stream)
+{
+    if (!plan)
+        return fail(GEMM_ERR_NULL_POINTER, "plan is NULL");
+    const gemm_xent_desc_t &d = plan->d;
+    const hipStream_t s = (hipStream_t)stream;
+    XentArgs a{};
+    XentPiece p{};
+    float *acc;
+    uint16_t *copy = nullptr;
+    if (d.tokens == 0)
+        return ok();
+    const int64_t bytes = (int64_t)xent_parts(*plan, false, workspace, a, p, acc, copy);
+    CHECK(check_buffers({{"X", X, d.tokens, d.hidden, d.ldx, 2, false},
+                         {"W", W, d.vocab, d.hidden, d.ldw, 2, false},
+                         {"targets", targets, d.tokens, 1, 1, d.id_bytes, false},
+                         {"loss", loss, loss ? d.tokens : 0, 1, 1, 4, true},
+                         {"lse", lse, d.tokens, 1, 1, 4, true},
+                         {"workspace", workspace, bytes, 1, 1, 1, true, 16}}));
+    CHECK(check_call(*plan, W));
+    fill_args(a, *plan, X, targets);
+    a.loss = loss;
+    a.lse = lse;
+    LAUNCH(launch_xent_prepare(a, false, s));
+    const int64_t step = plan->copy ? plan->piece : d.vocab;
+    for (p.v0 = 0; p.v0 < d.vocab; p.v0 += step) {
+        p.n = d.vocab - p.v0 < step ? d.vocab - p.v0 : step;
+        LAUNCH(take_w(*plan, W, copy, p, s));
+        LAUNCH(launch_xent_stats(plan->stats, a, p, s));
+        p.tile0 += ceil_div(p.n, xent_edge(plan->stats));
+    }
+    return launched(launch_xent_loss(a, s));
+}
+
+gemm_status_t gemm_xent_backward(const gemm_xent_plan_t *plan, const void *X, const void *W,
+                                 const void *targets, const float *lse, const float *dloss,
+                                 const float *dlse, void *dX, void *dW, void *workspace,
+                                 gemm_stream_t stream)
+{
+    if (!plan)
+        return fail(GEMM_ERR_NULL_POINTER, "plan is NULL");
+    const gemm_xent_desc_t &d = plan->d;
+    const hipStream_t s = (hipStream_t)stream;
+    XentArgs a{};
+    XentPiece p{};
+    float *acc = nullptr;
+    uint16_t *copy = nullptr;
+    const int64_t t = d.tokens, bytes = (int64_t)xent_parts(*plan, true, workspace, a, p, acc, copy);
+    const int64_t wb = float_bytes(d.dw_type);
+    CHECK(check_buffers({{"X", X, t, d.hidden, d.ldx, 2, false},
+                         {"W", W, d.vocab, d.hidden, d.ldw, 2, false},
+                         {"targets", targets, t, 1, 1, d.id_bytes, false},
+                         {"lse", lse, t, 1, 1, 4, false},
+                         {"dloss", dloss, t, 1, 1, 4, false},
+                         {"dlse", dlse, dlse ? t : 0, 1, 1, 4, false},
+                         {"dX", dX, dX ? t : 0, d.hidden, d.lddx, float_bytes(d.dx_type), true},
+                         {"dW", dW, dW ? d.vocab : 0, d.hidden, d.lddw, wb, true},
+                         {"workspace", workspace, bytes, 1, 1, 1, true, 16}}));
+    CHECK(check_call(*plan, W));
+    if (!dX && !dW)
+        return ok();
+    fill_args(a, *plan, X, targets);
+    a.lse_in = lse;
+    a.dloss = dloss;
+    a.dlse = dlse;
+    LAUNCH(launch_xent_prepare(a, true, s));
+    for (p.v0 = 0; p.v0 < d.vocab; p.v0 += plan->piece) {
+        p.n = d.vocab - p.v0 < plan->piece ? d.vocab - p.v0 : plan->piece;
+        LAUNCH(take_w(*plan, W, copy, p, s));
+        if (t > 0)
+            LAUNCH(launch_xent_g(plan->g, a, p, s));
+        if (dX && t > 0) {
+            const int64_t k = ceil_div(ceil_div(p.n, plan->dx_splits), 64) * 64;
+            LAUNCH(launch_xent_dx(plan->dx, a, p, {acc, (int)plan->dx_splits, k, p.v0 > 0}, s));
+        }
+        if (dW) {
+            uint8_t *w = (uint8_t *)dW + p.v0 * d.lddw * wb;
+            // the vector epilogue addresses 257 rows of dW with 32-bit offsets
+            const int vec = aligned(w, 4 * (size_t)wb) && d.lddw % 4 == 0 &&
+                            d.lddw * wb < 0x7fffffff / 257;
+            const int lines = aligned(w, 128) && (d.lddw * wb) % 128 == 0;
+            LAUNCH(launch_xent_dw(plan->dw, a, p,
+                                  {w, d.lddw, out_kind(d.dw_type), d.accumulate, vec, lines}, s));
+        }
+    }
+    if (dX && t > 0)
+        LAUNCH(launch_xent_out(a, {acc, (int)plan->dx_splits, dX, d.lddx, out_kind(d.dx_type)}, s));
+    return ok();
+}
+
+} // extern "C"

@@ -1,0 +1,125 @@
+// Argument blocks and launchers of the operators over a vocabulary
+// (vocab_api.cpp calls them; kernels_embed.hip and kernels_xent*.hip define
+// them).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kernel_args.hpp"
+
+namespace stg {
+
+// ---------------------------------------------------------------- embedding
+
+constexpr int64_t EMBED_MAX_VOCAB = (int64_t)1 << 20;
+// up to this many tokens the gradient is one launch, without a sort
+constexpr int EMBED_SMALL = 1024;
+// sorted positions whose rows one wave sums
+constexpr int EMBED_RUN = 32;
+constexpr int EMBED_MAX_BINS = 1024; // of either pass of the sort
+
+struct EmbedArgs {
+    int64_t tokens, vocab, cols;
+    int id8;
+    const void *ids;
+    int e_kind, y_kind; // OutKind: of the table (its gradient), of Y (dY)
+    const void *in;     // E; backward: dY
+    int64_t ld_in;
+    void *out; // Y; backward: dE
+    int64_t ld_out;
+    float scale;
+    int accumulate;
+    // backward, more than EMBED_SMALL tokens (the workspace): ids are cut into
+    // low bits (the first pass) and high ones (the second)
+    int lo_bits, hi_bits;
+    int chunk, chunks;    // tokens per workgroup of the first pass
+    int32_t *counts;      // [chunks][1 << lo_bits]
+    int32_t *bounds;      // [(1 << lo_bits) + 1] first place of each bin
+    int32_t *binned;      // [tokens] tokens by low bits
+    int32_t *order, *key; // [tokens] tokens by id, and their ids
+    float *part;          // [runs][2][cols] sums that go on in another run
+};
+
+hipError_t launch_embed(const EmbedArgs &a, hipStream_t s);
+hipError_t launch_embed_backward(const EmbedArgs &a, hipStream_t s);
+
+// ---------------------------------------------------------------- linear cross entropy
+
+// Workgroup tiles of a product.
+enum XentTile { XT_64 = 0, XT_128, XT_256, XT_COUNT };
+inline int xent_edge(int t) { return t == XT_256 ? 256 : t == XT_128 ? 128 : 64; }
+
+// tokens of a workgroup of the preparing kernel
+constexpr int XENT_PREP = 32;
+
+struct XentArgs {
+    int64_t tokens, vocab, hidden, hp; // hp: hidden in whole 16-byte chunks
+    int id8, bf16;
+    const void *X, *targets;
+    int64_t ldx;
+    float scale;
+    const float *lse_in, *dloss, *dlse; // backward
+    float *loss, *lse;                  // forward
+    // the workspace: rows are the tokens with a target, in order
+    int32_t *count;       // rows
+    int32_t *pos, *map;   // row of a token (-1: none), token of a row
+    int32_t *tgt;         // target of a row
+    float *ca, *cb, *cl;  // of a row: dloss + dlse, dloss, lse / ln 2
+    float *gmax;          // largest |ca|, |cb| of each workgroup's tokens
+    int64_t gmaxes;
+    uint16_t *Xc;         // rows x hp
+    float *zt;            // target's logit of a row
+    float *part;          // [tile column][row] maximum and sum
+    int64_t part_tiles;
+};
+
+// One piece of the vocabulary: columns v0 .. v0 + n - 1.
+struct XentPiece {
+    const void *W; // its first row, 16-byte aligned
+    int64_t ldw;
+    int64_t v0, n;
+    int64_t tile0; // forward: its first tile column in XentArgs::part
+    uint16_t *G;   // backward: rows x ldg
+    int64_t ldg;
+};
+
+// W's rows v0 .. v0 + n - 1 (hidden values each) to out (hp each, zeros at
+// the end)
+struct XentCopy {
+    const uint16_t *W;
+    int64_t ldw, n, hidden, hp;
+    uint16_t *out;
+};
+
+struct XentDx { // acc[split] (+)= G W
+    float *acc;  // [splits][tokens][hp]
+    int splits;
+    int64_t k_split; // columns of the piece per split, a multiple of 64
+    int add;         // add to what acc holds
+};
+struct XentDw {
+    void *dW; // the piece's first row
+    int64_t ldd;
+    int d_kind, add, vec, whole_lines;
+};
+struct XentOut { // dX = the sum of acc, scaled, by token
+    const float *acc;
+    int splits;
+    void *dX;
+    int64_t ldd;
+    int d_kind;
+};
+
+hipError_t launch_xent_prepare(const XentArgs &a, bool backward, hipStream_t s);
+hipError_t launch_xent_copy(const XentCopy &c, hipStream_t s);
+hipError_t launch_xent_stats(int tile, const XentArgs &a, const XentPiece &p, hipStream_t s);
+hipError_t launch_xent_loss(const XentArgs &a, hipStream_t s);
+hipError_t launch_xent_g(int tile, const XentArgs &a, const XentPiece &p, hipStream_t s);
+hipError_t launch_xent_dx(int tile, const XentArgs &a, const XentPiece &p, const XentDx &d,
+                          hipStream_t s);
+hipError_t launch_xent_dw(int tile, const XentArgs &a, const XentPiece &p, const XentDw &d,
+                          hipStream_t s);
+hipError_t launch_xent_out(const XentArgs &a, const XentOut &o, hipStream_t s);
+
+} // namespace stg

@@ -1,4 +1,4 @@
-"""Python binding of libstgemm.so (include/gemm.h, include/gemm_moe.h).  Argument marshalling only:
+"""Python binding of libstgemm.so (include/gemm.h, include/gemm_moe.h, include/gemm_vocab.h).  Argument marshalling only:
 every step of the computation runs in the library's HIP kernels.  Device
 buffers are passed as torch tensors (their data pointers) or raw integer
 addresses; PyTorch provides memory and streams only.
@@ -9,8 +9,12 @@ gemm_sparse24_compress, gemm_sparse24_compress_noalloc, gemm_sparse24_run, gemm_
 gemm_last_error, and from gemm_moe.h gemm_moe_sort_workspace,
 gemm_moe_sort, gemm_moe_dispatch, gemm_moe_combine, gemm_moe_combine_backward,
 gemm_grouped_validate_desc, gemm_grouped_plan, gemm_grouped_run,
-gemm_q8_store, gemm_q8_load, gemm_swiglu, gemm_swiglu_backward.  Non-OK statuses raise GemmError (except
-gemm_validate_desc, which returns the status).
+gemm_q8_store, gemm_q8_load, gemm_swiglu, gemm_swiglu_backward, and from
+gemm_vocab.h gemm_embed, gemm_embed_workspace, gemm_embed_backward,
+gemm_xent_validate_desc, gemm_xent_plan, gemm_xent_workspace,
+gemm_xent_forward, gemm_xent_backward.  Non-OK statuses raise GemmError (except
+those of gemm_validate_desc, gemm_grouped_validate_desc and
+gemm_xent_validate_desc, which return the status).
 """
 import ctypes
 import os
@@ -72,6 +76,17 @@ class gemm_grouped_desc_t(ctypes.Structure):
     ]
 
 
+class gemm_xent_desc_t(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("hidden", ctypes.c_int64),
+        ("x_type", ctypes.c_int32), ("dx_type", ctypes.c_int32), ("dw_type", ctypes.c_int32),
+        ("id_bytes", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("unaligned", ctypes.c_int32),
+        ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64),
+        ("lddx", ctypes.c_int64), ("lddw", ctypes.c_int64),
+        ("piece", ctypes.c_int64), ("scale", ctypes.c_float),
+    ]
+
+
 _lib = None
 
 
@@ -88,7 +103,9 @@ def load():
     st = ctypes.c_int
     dp = ctypes.POINTER(gemm_desc_t)
     gdp = ctypes.POINTER(gemm_grouped_desc_t)
+    xdp = ctypes.POINTER(gemm_xent_desc_t)
     sz = ctypes.POINTER(ctypes.c_size_t)
+    f32 = ctypes.c_float
     sig = {
         "gemm_validate_desc": (st, [dp]),
         "gemm_plan": (st, [dp, ctypes.POINTER(vp)]),
@@ -118,6 +135,17 @@ def load():
         "gemm_q8_load": (st, [i64, i64, i32, vp, vp, vp, i64, vp]),
         "gemm_swiglu": (st, [i64, i64, i32, vp, i64, vp, i64, vp, vp, vp]),
         "gemm_swiglu_backward": (st, [i64, i64, i32, vp, vp, vp, i64, vp, i64, vp, i64, vp]),
+        "gemm_embed": (st, [i64, i64, i64, i32, i32, i32, vp, vp, i64, vp, i64, f32, vp]),
+        "gemm_embed_workspace": (st, [i64, i64, i64, sz]),
+        "gemm_embed_backward": (st, [i64, i64, i64, i32, i32, i32, vp, vp, i64, vp, i64, i32, vp,
+                                     f32, vp]),
+        "gemm_xent_validate_desc": (st, [xdp]),
+        "gemm_xent_plan": (st, [xdp, ctypes.POINTER(vp)]),
+        "gemm_xent_plan_destroy": (st, [vp]),
+        "gemm_xent_plan_describe": (st, [vp, ctypes.c_char_p, ctypes.c_size_t]),
+        "gemm_xent_workspace": (st, [vp, sz, sz]),
+        "gemm_xent_forward": (st, [vp, vp, vp, vp, vp, vp, vp, vp]),
+        "gemm_xent_backward": (st, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         "gemm_diag_mfma_loop": (st, [i32, i32, i64, vp, vp]),
         "gemm_status_string": (ctypes.c_char_p, [st]),
         "gemm_last_error": (ctypes.c_char_p, []),
@@ -298,6 +326,17 @@ def _call(address, *args):
     return _call(address, *args)
 
 
+def _call_float(address, *args):
+    """The same for a function with one float among its arguments."""
+    global _call_float
+    try:
+        from . import _pycall
+    except ImportError as e:
+        raise RuntimeError("_pycall.so is not built; run `python -m sparse_tiled_gemm_amd.build`") from e
+    _call_float = _pycall.call_float
+    return _call_float(address, *args)
+
+
 def gemm_moe_sort_workspace(tokens, topk, groups):
     """Bytes of workspace of gemm_moe_sort and gemm_moe_dispatch."""
     n = ctypes.c_size_t()
@@ -409,6 +448,99 @@ def gemm_swiglu_backward(rows, cols, dtype, codes, scales, dH, lddh, dGU, lddgu,
     _check(_call(_at["gemm_swiglu_backward"], rows, cols, DTYPES[dtype], codes, scales,
                                        dH, lddh, dGU, lddgu, H, ldh,
                                        _stream(stream)))
+
+
+# ---------------------------------------------------------------- gemm_vocab.h
+# Argument order is the C functions', with keywords behind; a leading
+# dimension of 0 means packed.
+
+def gemm_embed(tokens, vocab, cols, e_dtype, y_dtype, ids, E, lde, Y, ldy, scale=1.0, id_bytes=4,
+               stream=None):
+    _check(_call_float(_at["gemm_embed"], tokens, vocab, cols, DTYPES[e_dtype], DTYPES[y_dtype],
+                       id_bytes, ids, E, lde, Y, ldy, float(scale), _stream(stream)))
+
+
+def gemm_embed_workspace(tokens, vocab, cols):
+    """Bytes of workspace of gemm_embed_backward."""
+    n = ctypes.c_size_t()
+    _check(load().gemm_embed_workspace(tokens, vocab, cols, ctypes.byref(n)))
+    return n.value
+
+
+def gemm_embed_backward(tokens, vocab, cols, y_dtype, e_dtype, ids, dY, lddy, dE, ldde, workspace,
+                        scale=1.0, accumulate=False, id_bytes=4, stream=None):
+    _check(_call_float(_at["gemm_embed_backward"], tokens, vocab, cols, DTYPES[y_dtype],
+                       DTYPES[e_dtype], id_bytes, ids, dY, lddy, dE, ldde, int(bool(accumulate)),
+                       workspace, float(scale), _stream(stream)))
+
+
+def make_xent_desc(tokens, vocab, hidden, dtype, dx_dtype=None, dw_dtype=None, *, scale=1.0,
+                   accumulate=False, id_bytes=4, unaligned=False, ldx=0, ldw=0, lddx=0, lddw=0,
+                   piece=0):
+    """Build a gemm_xent_desc_t; dx_dtype and dw_dtype default to dtype, that
+    of X and W."""
+    d = gemm_xent_desc_t()
+    d.tokens, d.vocab, d.hidden = tokens, vocab, hidden
+    d.x_type = DTYPES[dtype]
+    d.dx_type, d.dw_type = DTYPES[dx_dtype or dtype], DTYPES[dw_dtype or dtype]
+    d.id_bytes = id_bytes
+    d.accumulate, d.unaligned = int(bool(accumulate)), int(bool(unaligned))
+    d.ldx, d.ldw, d.lddx, d.lddw = ldx, ldw, lddx, lddw
+    d.piece, d.scale = piece, scale
+    return d
+
+
+def gemm_xent_validate_desc(desc):
+    """Returns the status code (GEMM_OK or an error); never raises."""
+    return load().gemm_xent_validate_desc(ctypes.byref(desc) if desc is not None else None)
+
+
+class XentPlan:
+    """Owns a gemm_xent_plan_t*; released by close()."""
+
+    def __init__(self, handle, desc):
+        self.handle = handle
+        self.desc = desc
+
+    def close(self):
+        if self.handle:
+            load().gemm_xent_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def name(self):
+        buf = ctypes.create_string_buffer(128)
+        _check(load().gemm_xent_plan_describe(self.handle, buf, len(buf)))
+        return buf.value.decode()
+
+
+def gemm_xent_plan(desc):
+    h = ctypes.c_void_p()
+    _check(load().gemm_xent_plan(ctypes.byref(desc), ctypes.byref(h)))
+    return XentPlan(h.value, desc)
+
+
+def gemm_xent_workspace(plan):
+    """Bytes of workspace of gemm_xent_forward and of gemm_xent_backward."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().gemm_xent_workspace(plan.handle, ctypes.byref(f), ctypes.byref(b)))
+    return f.value, b.value
+
+
+def gemm_xent_forward(plan, X, W, targets, loss, lse, workspace, stream=None):
+    _check(_call(_at["gemm_xent_forward"], plan.handle, X, W, targets, loss, lse, workspace,
+                 _stream(stream)))
+
+
+def gemm_xent_backward(plan, X, W, targets, lse, dloss, dlse, dX, dW, workspace, stream=None):
+    _check(_call(_at["gemm_xent_backward"], plan.handle, X, W, targets, lse, dloss, dlse, dX, dW,
+                 workspace, _stream(stream)))
 
 
 def gemm_diag_mfma_loop(kind, blocks, iters, out, stream=None):
