@@ -43,7 +43,7 @@ extern "C" {
  *
  * E: vocab x cols, Y: tokens x cols; types GEMM_F16, GEMM_BF16 or GEMM_F32,
  * in any combination.  Pointers need the alignment of their elements only.
- * tokens at most 2^26, vocab at most 2^20, cols at most 2^23
+ * tokens at most 2^25, vocab at most 2^20, cols at most 2^23
  * (GEMM_ERR_UNSUPPORTED above). */
 
 /* Enqueue Y[t] = cast(scale * E[ids[t]]) (fp32 product, rounded once), zeros

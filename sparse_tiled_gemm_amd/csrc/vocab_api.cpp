@@ -37,8 +37,8 @@ gemm_status_t check_embed(int64_t tokens, int64_t vocab, int64_t cols)
 {
     if (tokens < 0 || vocab < 0 || cols < 0)
         return fail(GEMM_ERR_INVALID_VALUE, "negative size");
-    if (tokens > (1 << 26) || vocab > EMBED_MAX_VOCAB || cols > (1 << 23))
-        return fail(GEMM_ERR_UNSUPPORTED, "at most 2^26 tokens, 2^20 rows and 2^23 columns");
+    if (tokens > (1 << 25) || vocab > EMBED_MAX_VOCAB || cols > (1 << 23))
+        return fail(GEMM_ERR_UNSUPPORTED, "at most 2^25 tokens, 2^20 rows and 2^23 columns");
     return GEMM_OK;
 }
 

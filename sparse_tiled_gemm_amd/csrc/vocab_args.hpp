@@ -36,7 +36,9 @@ struct EmbedArgs {
     int chunk, chunks;    // tokens per workgroup of the first pass
     int32_t *counts;      // [chunks][1 << lo_bits]
     int32_t *bounds;      // [(1 << lo_bits) + 1] first place of each bin
-    int32_t *binned;      // [tokens] tokens by low bits
+    struct Binned {
+        int32_t id, token;
+    } *binned;            // [tokens] tokens by low bits
     int32_t *order, *key; // [tokens] tokens by id, and their ids
     float *part;          // [runs][2][cols] sums that go on in another run
 };

@@ -1,21 +1,15 @@
 // Pieces shared by the kernels of the linear cross entropy.
 #pragma once
-#include "device_common.hpp"
-#include "vocab_args.hpp"
+#include "vocab_id.hpp"
 
 namespace stg {
 
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
+// Token t's target, -1: none.
 __device__ STG_AI inline int xent_target(const XentArgs &a, int64_t t)
 {
-    // -1: none
-    if (a.id8) {
-        const int64_t v = ((const int64_t *)a.targets)[t];
-        return v >= 0 && v < a.vocab ? (int)v : -1;
-    }
-    const int32_t v = ((const int32_t *)a.targets)[t];
-    return v >= 0 && v < a.vocab ? v : -1;
+    return vocab_id(a.targets, a.id8, a.vocab, t);
 }
 
 // The logits' gradient enters its products as a 16-bit value relative to the

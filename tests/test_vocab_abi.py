@@ -29,7 +29,7 @@ EMBED = dict(tokens=8, vocab=100, cols=64, e_dtype="bf16", y_dtype="f16", ids=P(
 
 @pytest.mark.parametrize("change,status", [
     (dict(tokens=-1), INVALID), (dict(vocab=-1), INVALID), (dict(cols=-1), INVALID),
-    (dict(tokens=(1 << 26) + 1), UNSUPPORTED), (dict(vocab=(1 << 20) + 1), UNSUPPORTED),
+    (dict(tokens=(1 << 25) + 1), UNSUPPORTED), (dict(vocab=(1 << 20) + 1), UNSUPPORTED),
     (dict(cols=(1 << 23) + 1), UNSUPPORTED), (dict(e_dtype="s8"), UNSUPPORTED),
     (dict(y_dtype="e4m3"), UNSUPPORTED), (dict(id_bytes=2), INVALID), (dict(lde=63), INVALID),
     (dict(ldy=-64), INVALID), (dict(ldy=1 << 41), INVALID), (dict(ids=None), NULL),
@@ -83,7 +83,7 @@ def test_embed_workspace():
     n = G.gemm_embed_workspace(65536, 131072, 4096)
     # two fp32 rows per 32 tokens, three ints per token, the counts
     assert 65536 // 32 * 2 * 4096 * 4 <= n <= 65536 // 32 * 2 * 4096 * 4 + 16 * 65536 + 4 * 64 * 1024
-    for bad in [(-1, 1, 1), (1, (1 << 20) + 1, 1), (1, 1, -1), ((1 << 26) + 1, 1, 1)]:
+    for bad in [(-1, 1, 1), (1, (1 << 20) + 1, 1), (1, 1, -1), ((1 << 25) + 1, 1, 1)]:
         with pytest.raises(G.GemmError):
             G.gemm_embed_workspace(*bad)
     assert G.load().gemm_embed_workspace(1, 1, 1, None) == NULL
