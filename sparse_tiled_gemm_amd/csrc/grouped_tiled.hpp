@@ -300,7 +300,7 @@ struct SmallShape {
 };
 
 // The operands of the tile of group t at (m_blk, n_blk); M, K: its group's
-// rows (of the output) and sum; KB: an MN-major B's K rows, if fewer exist.
+// rows (of the output) and sum; KB: an MN-major operand's K rows, if fewer exist.
 template <class S>
 __device__ STG_AI inline void set_operands(typename S::OpA &A, typename S::OpB &B,
                                            const GroupedArgs &a, const GroupRows &t, int64_t m_blk,
@@ -314,7 +314,7 @@ __device__ STG_AI inline void set_operands(typename S::OpA &A, typename S::OpB &
         A.span = M - m_blk;
     } else {
         A.base = (const uint8_t *)a.A + t.r0 * A.ld + m_blk * 2;
-        A.k_bytes = K;
+        A.k_bytes = KB;
         A.span = (M - m_blk) * 2;
     }
     constexpr int BE = S::BLAY == GL_Q8 ? 1 : 2;

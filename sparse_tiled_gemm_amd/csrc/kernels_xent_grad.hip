@@ -20,10 +20,11 @@ struct DxTile {
 };
 // Operands of split `split` of dX's product; K 0: nothing to add.
 __device__ STG_AI inline DxTile dx_tile(const XentArgs &a, const XentPiece &p, const XentDx &d, int n,
-                                        int split)
+                                        int split, int splits)
 {
     DxTile x{};
-    const int64_t k0 = split * d.k_split, kb = min(d.k_split, p.n - k0);
+    const int64_t per = ((p.n + splits - 1) / splits + 63) / 64 * 64;
+    const int64_t k0 = split * per, kb = min(per, p.n - k0);
     x.KB = kb > 0 ? kb : 0;
     x.K = chunks8(x.KB);
     x.g.N = a.hp;
@@ -36,7 +37,7 @@ __device__ STG_AI inline DxTile dx_tile(const XentArgs &a, const XentPiece &p, c
     x.e.N = a.hp;
     x.e.alpha = 1.0f;
     x.e.d_kind = OUT_F32;
-    x.e.D = d.acc + split * a.tokens * a.hp;
+    x.e.D = d.acc + (int64_t)split * n * a.hp;
     x.e.ldd = x.e.ldc = a.hp;
     x.e.C = d.add ? x.e.D : nullptr;
     x.e.vec = 1;
@@ -84,18 +85,20 @@ k_xent_grad(XentArgs a, XentPiece p, XentDx dx, XentDw dw, int tiles_n)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = __builtin_amdgcn_readfirstlane(*a.count);
     const int tiles_m = (int)(((DW ? p.n : (int64_t)n) + BM - 1) / BM);
-    const int id = xcd_tile(blockIdx.x, tiles_m * tiles_n);
+    const int tiles = tiles_m * tiles_n, splits = DW ? 1 : __builtin_amdgcn_readfirstlane(a.count[1]);
+    const int id = xcd_tile(blockIdx.x, tiles * splits);
     if (id < 0)
         return;
     int tm, tn;
-    tile_of(id, tiles_m, tiles_n, tm, tn);
+    tile_of(id % tiles, tiles_m, tiles_n, tm, tn);
     const int64_t m = wave_uniform((int64_t)tm * BM), c = wave_uniform((int64_t)tn * BN);
     typename OP::acc_t acc[S::FM][S::FN];
     const GroupRows t = {0, 0, n, 0};
     if constexpr (DW) {
         const GroupedArgs g = dw_args(a, p);
+        const Gmax first = load_gmax(a, lane); // (nothing waits for it later)
         tile_sum<OP, true, GL_MN, GL_MN, BM, BN>(g, t, m, c, g.K, n, n, lane, wave, L, acc);
-        const float f = xent_factor(a, lane);
+        const float f = xent_factor(a, first, lane);
 #pragma unroll
         for (int i = 0; i < S::FM; ++i)
 #pragma unroll
@@ -104,7 +107,7 @@ k_xent_grad(XentArgs a, XentPiece p, XentDx dx, XentDw dw, int tiles_n)
         store_acc<OP, S>(dw_epilogue(a, p, dw), dw.whole_lines, m, c, acc, lane, wave,
                          wave_slab(L, wave));
     } else {
-        const DxTile x = dx_tile(a, p, dx, n, blockIdx.y);
+        const DxTile x = dx_tile(a, p, dx, n, id / tiles, splits);
         if (x.K == 0 && dx.add)
             return;
         tile_sum<OP, false, GL_K, GL_MN, BM, BN>(x.g, t, m, c, n, x.K, x.KB, lane, wave, L, acc);
@@ -123,19 +126,21 @@ __global__ __launch_bounds__(256, 2) void k_xent_grad_small(XentArgs a, XentPiec
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = __builtin_amdgcn_readfirstlane(*a.count);
     const int tiles_m = (int)(((DW ? p.n : (int64_t)n) + 63) / 64);
-    const int id = xcd_tile(blockIdx.x, tiles_m * tiles_n);
+    const int tiles = tiles_m * tiles_n, splits = DW ? 1 : __builtin_amdgcn_readfirstlane(a.count[1]);
+    const int id = xcd_tile(blockIdx.x, tiles * splits);
     if (id < 0)
         return;
     int tm, tn;
-    tile_of(id, tiles_m, tiles_n, tm, tn);
+    tile_of(id % tiles, tiles_m, tiles_n, tm, tn);
     const int64_t m = wave_uniform((int64_t)tm * 64), c = wave_uniform((int64_t)tn * 64);
     typename OP::acc_t acc[2][2];
     const GroupRows t = {0, 0, n, 0};
     uint8_t *slab = wave == 0 ? s0 : wave == 1 ? s1 : wave == 2 ? s2 : s3;
     if constexpr (DW) {
         const GroupedArgs g = dw_args(a, p);
+        const Gmax first = load_gmax(a, lane);
         small_sum<OP, true, GL_MN, GL_MN>(g, t, m, c, g.K, n, n, lane, wave, s0, s1, s2, s3, acc);
-        const float f = xent_factor(a, lane);
+        const float f = xent_factor(a, first, lane);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -144,7 +149,7 @@ __global__ __launch_bounds__(256, 2) void k_xent_grad_small(XentArgs a, XentPiec
         store_acc<OP, S>(dw_epilogue(a, p, dw), dw.whole_lines, m, c, acc, lane, wave,
                          (uint32_t *)slab);
     } else {
-        const DxTile x = dx_tile(a, p, dx, n, blockIdx.y);
+        const DxTile x = dx_tile(a, p, dx, n, id / tiles, splits);
         if (x.K == 0 && dx.add)
             return;
         small_sum<OP, false, GL_K, GL_MN>(x.g, t, m, c, n, x.K, x.KB, lane, wave, s0, s1, s2, s3, acc);
@@ -156,9 +161,10 @@ template <class OP, bool DW>
 static hipError_t launch_t(int tile, const XentArgs &a, const XentPiece &p, const XentDx &dx,
                            const XentDw &dw, hipStream_t s)
 {
-    const int64_t b = xent_edge(tile), m = DW ? p.n : a.tokens;
+    const int64_t b = xent_edge(tile);
     const int tiles_n = (int)((a.hp + b - 1) / b);
-    const dim3 grid((unsigned)(((m + b - 1) / b * tiles_n + 7) / 8 * 8), DW ? 1 : dx.splits);
+    const int64_t wgs = DW ? (p.n + b - 1) / b * tiles_n : a.dx.wgs;
+    const dim3 grid((unsigned)((wgs + 7) / 8 * 8));
     if (tile == XT_256)
         hipLaunchKernelGGL((k_xent_grad<OP, DW, 256, 256>), grid, dim3(512), 0, s, a, p, dx, dw,
                            tiles_n);

@@ -33,45 +33,92 @@ __device__ STG_AI inline float sum16(float x)
     return x + dpp<0x140>(x);
 }
 
+// x in the places of the tile's columns behind the piece's last one; col: the
+// lane's first column in the tile.
+template <class OP, class S>
+__device__ STG_AI inline void mask_columns(const XentPiece &p, int64_t n_blk, int col,
+                                           typename OP::acc_t (&acc)[S::FM][S::FN], float x)
+{
+    if (n_blk + S::BN <= p.n)
+        return;
+    const int left = (int)(p.n - n_blk) - col;
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j)
+        if (16 * j >= left)
+#pragma unroll
+            for (int i = 0; i < S::FM; ++i)
+                acc[i][j] = typename OP::acc_t{x, x, x, x};
+}
+
+// What the tile's epilogue needs of the row of thread tid (the first BM of a
+// workgroup), loaded before the tile's sums so that nothing waits for it.
+struct RowVals {
+    int tgt; // target relative to the tile's columns
+    float ca, cb, cl;
+    Gmax gmax;
+};
+template <bool GRAD, int BM>
+__device__ STG_AI inline RowVals load_row(const XentArgs &a, const XentPiece &p, int n, int64_t m_blk,
+                                          int64_t n_blk, int tid)
+{
+    const int64_t row = m_blk + tid;
+    RowVals v = {-1, 0.0f, 0.0f, 0.0f, {}};
+    if (tid < BM && row < n) {
+        v.tgt = (int)(xent_row_target(a, row) - (p.v0 + n_blk));
+        if constexpr (GRAD) {
+            v.ca = a.ca[row];
+            v.cb = a.cb[row];
+            v.cl = a.cl[row];
+        }
+    }
+    if constexpr (GRAD)
+        v.gmax = load_gmax(a, threadIdx.x & 63);
+    return v;
+}
+
 // Statistics of the tile at (m_blk, n_blk), tile column tn; n: rows.  lds: BM
 // ints, GN * BM pairs of floats (16-byte aligned).
 template <class OP, class S>
 __device__ STG_AI inline void tile_stats(const XentArgs &a, const XentPiece &p, int n, int64_t m_blk,
-                                         int64_t n_blk, int tn,
+                                         int64_t n_blk, int tn, const RowVals &row,
                                          typename OP::acc_t (&acc)[S::FM][S::FN], int lane, int wave,
                                          int *tgt, float *st)
 {
     static_assert(S::PA == 1 && S::PB == 1, "a wave's block is one piece");
     const int tid = threadIdx.x, l16 = lane & 15, q = lane >> 4;
     const int rb = wave / S::GN * S::WM, cb = wave % S::GN * S::WN;
-    if (tid < S::BM) // targets relative to the tile's columns
-        tgt[tid] = m_blk + tid < n ? (int)(a.tgt[m_blk + tid] - (p.v0 + n_blk)) : -1;
+    if (tid < S::BM)
+        tgt[tid] = row.tgt;
+    if (a.scale != 1.0f)
+#pragma unroll
+        for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < S::FN; ++j)
+                acc[i][j] *= a.scale;
+    mask_columns<OP, S>(p, n_blk, cb + l16, acc, -INFINITY);
     __syncthreads();
-    const int left = (int)min((int64_t)S::BN, p.n - n_blk) - cb - l16; // columns from this lane's on
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
         const i4_t tg = *(const i4_t *)(tgt + rb + 16 * i + 4 * q);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            float z[S::FN], m = -INFINITY, s = 0.0f;
+            float m = acc[i][0][r], s = 0.0f;
 #pragma unroll
-            for (int j = 0; j < S::FN; ++j) {
-                z[j] = 16 * j < left ? acc[i][j][r] * a.scale : -INFINITY;
-                m = __builtin_fmaxf(m, z[j]);
-            }
+            for (int j = 1; j < S::FN; ++j)
+                m = __builtin_fmaxf(m, acc[i][j][r]);
             const int d = tg[r] - cb - l16;
             if ((uint32_t)d < (uint32_t)S::WN && (d & 15) == 0) {
-                float x = z[0];
+                float x = acc[i][0][r];
 #pragma unroll
                 for (int j = 1; j < S::FN; ++j)
-                    x = d >> 4 == j ? z[j] : x;
+                    x = d >> 4 == j ? acc[i][j][r] : x;
                 a.zt[m_blk + rb + 16 * i + 4 * q + r] = x;
             }
             m = max16(m);
             const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
             for (int j = 0; j < S::FN; ++j)
-                s += __builtin_amdgcn_exp2f((z[j] - ref) * LOG2E);
+                s += __builtin_amdgcn_exp2f((acc[i][j][r] - ref) * LOG2E);
             s = sum16(s);
             if (l16 == 0) {
                 float *o = st + ((wave % S::GN) * S::BM + rb + 16 * i + 4 * q + r) * 2;
@@ -99,46 +146,43 @@ __device__ STG_AI inline void tile_stats(const XentArgs &a, const XentPiece &p, 
 
 // The tile's G in place of its sums.  rows: four arrays of BM values in LDS.
 template <class OP, class S>
-__device__ STG_AI inline void tile_g(const XentArgs &a, const XentPiece &p, int n, int64_t m_blk,
-                                     int64_t n_blk, typename OP::acc_t (&acc)[S::FM][S::FN], int lane,
-                                     int wave, float *rows)
+__device__ STG_AI inline void tile_g(const XentArgs &a, const XentPiece &p, int64_t n_blk,
+                                     const RowVals &row, typename OP::acc_t (&acc)[S::FM][S::FN],
+                                     int lane, int wave, float *rows)
 {
     static_assert(S::PA == 1 && S::PB == 1, "a wave's block is one piece");
     const int tid = threadIdx.x, l16 = lane & 15, q = lane >> 4;
     const int rb = wave / S::GN * S::WM, cb = wave % S::GN * S::WN;
-    const float gmax = xent_gmax(a, lane);
-    if (tid < S::BM) {
-        const int64_t row = m_blk + tid;
-        const bool in = row < n;
-        const float f = xent_unit(a);
-        // (gmax 0: every coefficient is)
-        rows[tid] = in && gmax != 0.0f ? a.ca[row] / gmax * f : 0.0f;
-        rows[S::BM + tid] = in && gmax != 0.0f ? a.cb[row] / gmax * f : 0.0f;
-        rows[2 * S::BM + tid] = in ? a.cl[row] : 0.0f;
-        ((int *)rows)[3 * S::BM + tid] = in ? (int)(a.tgt[row] - (p.v0 + n_blk)) : -1;
+    const float gmax = xent_gmax(a, row.gmax, lane), f = xent_unit(a);
+    if (tid < S::BM) { // (gmax 0: every coefficient is)
+        rows[tid] = gmax != 0.0f ? row.ca / gmax * f : 0.0f;
+        rows[S::BM + tid] = gmax != 0.0f ? row.cb / gmax * f : 0.0f;
+        rows[2 * S::BM + tid] = row.cl;
+        ((int *)rows)[3 * S::BM + tid] = row.tgt;
     }
     __syncthreads();
-    const int left = (int)min((int64_t)S::BN, p.n - n_blk) - cb - l16;
     const float k = a.scale * LOG2E;
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
         const float *at = rows + rb + 16 * i + 4 * q;
-        const f4_t ca = *(const f4_t *)at, cbv = *(const f4_t *)(at + S::BM);
-        const f4_t cl = *(const f4_t *)(at + 2 * S::BM);
+        const f4_t ca = *(const f4_t *)at, cl = *(const f4_t *)(at + 2 * S::BM);
         const i4_t tg = *(const i4_t *)(at + 3 * S::BM);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int d = tg[r] - cb - l16;
 #pragma unroll
-            for (int j = 0; j < S::FN; ++j) {
-                const float e =
-                    __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], k, -cl[r]));
-                float g = ca[r] * e;
-                g -= d == 16 * j ? cbv[r] : 0.0f;
-                acc[i][j][r] = 16 * j < left ? g : 0.0f;
+            for (int j = 0; j < S::FN; ++j)
+                acc[i][j][r] =
+                    ca[r] * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], k, -cl[r]));
+            const int d = tg[r] - cb - l16;
+            if ((uint32_t)d < (uint32_t)S::WN && (d & 15) == 0) {
+                const float x = at[S::BM + r];
+#pragma unroll
+                for (int j = 0; j < S::FN; ++j)
+                    acc[i][j][r] -= d >> 4 == j ? x : 0.0f;
             }
         }
     }
+    mask_columns<OP, S>(p, n_blk, cb + l16, acc, 0.0f);
     __syncthreads(); // the rows are read before LDS takes the slabs
 }
 
@@ -160,8 +204,8 @@ __device__ STG_AI inline GroupedArgs logits_args(const XentArgs &a, const XentPi
 {
     GroupedArgs g{};
     g.N = p.n;
-    g.A = a.Xc;
-    g.lda = a.hp;
+    g.A = a.direct ? a.X : a.Xc;
+    g.lda = a.direct ? a.ldx : a.hp;
     g.B = p.W;
     g.ldb = p.ldw;
     return g;
@@ -180,7 +224,7 @@ __global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_xent_tile
     static_assert(AB >= 4 * BM * 4 && AB >= S::GN * BM * 8, "rows' values");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = __builtin_amdgcn_readfirstlane(*a.count), tiles_m = (n + BM - 1) / BM;
+    const int n = xent_rows(a), tiles_m = (n + BM - 1) / BM;
     const int id = xcd_tile(blockIdx.x, tiles_m * tiles_n);
     if (id < 0)
         return;
@@ -189,13 +233,14 @@ __global__ __launch_bounds__(512, BM * BN >= 256 * 128 ? 2 : 4) void k_xent_tile
     const int64_t m = wave_uniform((int64_t)tm * BM), c = wave_uniform((int64_t)tn * BN);
     typename OP::acc_t acc[S::FM][S::FN];
     const GroupRows t = {0, 0, n, 0};
+    const RowVals row = load_row<GRAD, BM>(a, p, n, m, c, threadIdx.x);
     tile_sum<OP, false, GL_K, GL_K, BM, BN>(logits_args(a, p), t, m, c, n, a.hp, a.hp, lane, wave, L,
                                             acc);
     if constexpr (GRAD) {
-        tile_g<OP, S>(a, p, n, m, c, acc, lane, wave, (float *)a00);
+        tile_g<OP, S>(a, p, c, row, acc, lane, wave, (float *)a00);
         store_acc<OP, S>(g_epilogue(a, p, n), 0, m, c, acc, lane, wave, wave_slab(L, wave));
     } else {
-        tile_stats<OP, S>(a, p, n, m, c, tn, acc, lane, wave, (int *)a00, (float *)a10);
+        tile_stats<OP, S>(a, p, n, m, c, tn, row, acc, lane, wave, (int *)a00, (float *)a10);
     }
 }
 
@@ -206,7 +251,7 @@ __global__ __launch_bounds__(256, 2) void k_xent_small(XentArgs a, XentPiece p, 
     typedef SmallShape<OP, false, GL_K, GL_K> S;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = __builtin_amdgcn_readfirstlane(*a.count), tiles_m = (n + 63) / 64;
+    const int n = xent_rows(a), tiles_m = (n + 63) / 64;
     const int id = xcd_tile(blockIdx.x, tiles_m * tiles_n);
     if (id < 0)
         return;
@@ -215,20 +260,206 @@ __global__ __launch_bounds__(256, 2) void k_xent_small(XentArgs a, XentPiece p, 
     const int64_t m = wave_uniform((int64_t)tm * 64), c = wave_uniform((int64_t)tn * 64);
     typename OP::acc_t acc[2][2];
     const GroupRows t = {0, 0, n, 0};
+    const RowVals row = load_row<GRAD, 64>(a, p, n, m, c, threadIdx.x);
     small_sum<OP, false, GL_K, GL_K>(logits_args(a, p), t, m, c, n, a.hp, a.hp, lane, wave, s0, s1, s2,
                                      s3, acc);
     if constexpr (GRAD) {
-        tile_g<OP, S>(a, p, n, m, c, acc, lane, wave, (float *)s0);
+        tile_g<OP, S>(a, p, c, row, acc, lane, wave, (float *)s0);
         uint8_t *slab = wave == 0 ? s0 : wave == 1 ? s1 : wave == 2 ? s2 : s3;
         store_acc<OP, S>(g_epilogue(a, p, n), 0, m, c, acc, lane, wave, (uint32_t *)slab);
     } else {
-        tile_stats<OP, S>(a, p, n, m, c, tn, acc, lane, wave, (int *)s0, (float *)s1);
+        tile_stats<OP, S>(a, p, n, m, c, tn, row, acc, lane, wave, (int *)s0, (float *)s1);
+    }
+}
+
+// Up to 16 rows: W's stream is the time.  A wave takes groups of 16 columns in
+// turn and copies their K tiles (128 values of 16 columns, 4 KB, 256-byte runs)
+// into LDS buffers of its own, three ahead and on into the next group, so that
+// the stream stops neither for a barrier nor for an epilogue; X's fragments come
+// from L2 beside them.  The statistics are kept per lane while the groups pass,
+// the running maximum and the sum relative to it, and joined once at the end:
+// one pair per row and workgroup.  Every step has eight vector-memory
+// instructions (past the last one they load zeros without touching memory), so
+// a step's have arrived when 3 x 8 newer ones are left.  One row, 32768 x 2048
+// (128 MB not in the caches; a plain read of it takes 21 us): the pass 33.5 us,
+// with 64-value tiles and eight buffers 34.2, with five buffers 35.7, with 64 x
+// 64 tiles 37.0.
+constexpr int ST_BUF = 4;
+template <class OP, bool GRAD>
+__global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p, int groups)
+{
+    constexpr bool BF = std::is_same<OP, Op16BF16>::value;
+    __shared__ __attribute__((aligned(1024))) uint8_t b0[16384], b1[16384], b2[16384], b3[16384];
+    const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = gridDim.x * 4;
+    const int n = xent_rows(a), KT = (int)((a.hp + 127) / 128);
+    const int64_t kb = a.hp * 2, ldw = p.ldw * 2, lda = (a.direct ? a.ldx : a.hp) * 2;
+    const __amdgpu_buffer_rsrc_t ra =
+        tile_rsrc(a.direct ? a.X : a.Xc, n > 0 ? (n - 1) * lda + kb : 0);
+    auto buf = [&](auto slot) STG_AI {
+        constexpr int S = decltype(slot)::value;
+        return (S == 0 ? b0 : S == 1 ? b1 : S == 2 ? b2 : b3) + wave * 4096;
+    };
+    if (n == 0)
+        return;
+    // (row l16's values; past the end the last row's, unused)
+    const RowVals row = load_row<GRAD, 16>(a, p, n, 0, 0, min(l16, n - 1));
+    // the step whose copies are issued next, and the one that is multiplied
+    const int va = l16 * (int)lda + q * 16;
+    int ig = blockIdx.x * 4 + wave, it = 0;
+    u4_t fa[ST_BUF][4];
+    auto issue = [&](auto slot) STG_AI {
+        constexpr int S = decltype(slot)::value;
+        const bool in = ig < groups;
+        const int64_t c = (int64_t)ig * 16;
+        const __amdgpu_buffer_rsrc_t rb = epi_rsrc((const uint8_t *)p.W + (in ? c * ldw : 0),
+                                                   in ? (p.n - c - 1) * ldw + kb : 0);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int row = 4 * d + q, chunk = (l16 ^ row) * 16;
+            const bool kin = it * 256 + chunk < kb;
+            dma16(rb, buf(slot) + 1024 * d, kin ? row * (int)ldw + chunk : (int)0x80000000, it * 256);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const bool ain = in && it * 256 + 64 * k + q * 16 < kb;
+            fa[S][k] = buf_load16(ra, ain ? va + 64 * k : (int)0x80000000, it * 256);
+        }
+        if (++it == KT) {
+            it = 0;
+            ig += waves;
+        }
+    };
+    auto all = [&](auto &&f) STG_AI {
+        [&]<int... I>(std::integer_sequence<int, I...>) STG_AI {
+            (f(std::integral_constant<int, I>{}), ...);
+        }(std::make_integer_sequence<int, ST_BUF>{});
+    };
+    in_order();
+    all(issue);
+    in_order();
+    // rows 4 q .. 4 q + 3 are this lane's accumulators
+    float ca[4], cb[4], cl[4], m[4], s[4];
+    int tgt[4];
+    float gmax = 0.0f;
+    if constexpr (GRAD)
+        gmax = xent_gmax(a, row.gmax, lane);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        tgt[r] = __shfl(row.tgt, 4 * q + r);
+        tgt[r] = 4 * q + r < n ? tgt[r] : -1;
+        m[r] = -INFINITY;
+        s[r] = 0.0f;
+        if constexpr (GRAD) { // (gmax 0: every coefficient is)
+            const float f = xent_unit(a);
+            ca[r] = gmax != 0.0f ? __shfl(row.ca, 4 * q + r) / gmax * f : 0.0f;
+            cb[r] = gmax != 0.0f ? __shfl(row.cb, 4 * q + r) / gmax * f : 0.0f;
+            cl[r] = __shfl(row.cl, 4 * q + r);
+        }
+    }
+    int g = blockIdx.x * 4 + wave, t = 0;
+    // (four sums of a quarter of the values each: their roundings are smaller
+    // than one sum's, and no product waits for the one before)
+    typename OP::acc_t part[4] = {};
+    auto finish = [&]() STG_AI { // a group's logits: rows 4 q + r, column l16
+        const int col = g * 16 + l16;
+        const typename OP::acc_t acc = (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            part[k] = typename OP::acc_t{};
+        if (g >= groups)
+            return;
+        if constexpr (GRAD) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float x = ca[r] * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[r], a.scale * LOG2E, -cl[r]));
+                x -= tgt[r] == col ? cb[r] : 0.0f;
+                x = col < p.n ? x : 0.0f;
+                if (4 * q + r < n)
+                    p.G[(4 * q + r) * p.ldg + col] = BF ? f32_to_bf16_bits(x) : f32_to_f16_bits(x);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float z = acc[r] * a.scale;
+                if (tgt[r] == col)
+                    a.zt[4 * q + r] = z;
+                const float x = col < p.n ? z : -INFINITY, mx = __builtin_fmaxf(m[r], x);
+                const float ref = mx == -INFINITY ? 0.0f : mx;
+                s[r] = s[r] * __builtin_amdgcn_exp2f((m[r] - ref) * LOG2E) +
+                       __builtin_amdgcn_exp2f((x - ref) * LOG2E);
+                m[r] = mx;
+            }
+        }
+    };
+    auto step = [&](auto slot) STG_AI {
+        constexpr int S = decltype(slot)::value;
+        in_order();
+        STG_WAIT_VMCNT((ST_BUF - 1) * 8);
+        in_order();
+        u4_t fb[4], x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            fb[k] = *(const u4_t *)(buf(slot) + l16 * 256 + (((4 * k + q) ^ l16) << 4));
+            x[k] = fa[S][k];
+        }
+        wave_lds_sync(); // read before the buffer is copied into again
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            part[k] = OP::mma((const uint32_t *)&x[k], (const uint32_t *)&fb[k], part[k]);
+        in_order();
+        issue(slot);
+        in_order();
+        if (++t == KT) {
+            finish();
+            t = 0;
+            g += waves;
+        }
+    };
+    // (without conditions between the steps, from which the compiler would take
+    // that fewer loads may be in flight: those past the last group multiply zeros)
+    while (g < groups)
+        all(step);
+    STG_WAIT_VMCNT(0); // copies past the last step, before LDS is reused
+    if constexpr (!GRAD) {
+        __syncthreads();
+        float *st = (float *)b0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float mx = max16(m[r]), ref = mx == -INFINITY ? 0.0f : mx;
+            const float sum = sum16(s[r] * __builtin_amdgcn_exp2f((m[r] - ref) * LOG2E));
+            if (l16 == 0) {
+                st[(wave * 16 + 4 * q + r) * 2] = mx;
+                st[(wave * 16 + 4 * q + r) * 2 + 1] = sum;
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x < n) {
+            float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                mx = __builtin_fmaxf(mx, st[(w * 16 + threadIdx.x) * 2]);
+            const float ref = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                sum += st[(w * 16 + threadIdx.x) * 2 + 1] *
+                       __builtin_amdgcn_exp2f((st[(w * 16 + threadIdx.x) * 2] - ref) * LOG2E);
+            float *o = a.part + ((p.tile0 + blockIdx.x) * a.tokens + threadIdx.x) * 2;
+            o[0] = mx;
+            o[1] = sum;
+        }
     }
 }
 
 template <class OP, bool GRAD>
 static hipError_t launch_t(int tile, const XentArgs &a, const XentPiece &p, hipStream_t s)
 {
+    if (tile == XT_STREAM) {
+        hipLaunchKernelGGL((k_xent_stream<OP, GRAD>), dim3((unsigned)xent_streams(p.n, a.dx.num_cu)),
+                           dim3(256), 0, s, a, p, (int)((p.n + 15) / 16));
+        return hipGetLastError();
+    }
     const int64_t b = xent_edge(tile);
     const int tiles_n = (int)((p.n + b - 1) / b);
     const dim3 grid((unsigned)(((a.tokens + b - 1) / b * tiles_n + 7) / 8 * 8));

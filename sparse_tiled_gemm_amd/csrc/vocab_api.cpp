@@ -20,7 +20,8 @@ struct gemm_xent_plan {
     int copy;           // W goes through the workspace
     int stats, g, dx, dw; // XentTile of each product
     int64_t piece;      // columns of a piece
-    int64_t dx_splits;  // parts of a piece whose sums dX's product keeps apart
+    XentSplits split;   // of dX's sums, by the rows that have a target
+    int64_t acc;        // fp32 values that they take
     int device;
     char name[96];
 };
@@ -208,8 +209,8 @@ gemm_status_t gemm_xent_validate_desc(const gemm_xent_desc_t *desc)
     for (int64_t ld : {d.ldx, d.ldw, d.lddx, d.lddw})
         if (ld > MAX_ELEMS || smul(d.tokens > d.vocab ? d.tokens : d.vocab, ld) > MAX_ELEMS)
             return fail(GEMM_ERR_INVALID_VALUE, "a matrix spans more than 2^40 elements");
-    if (d.tokens > (1 << 24) || d.vocab > (1 << 24) || d.hidden > (1 << 20))
-        return fail(GEMM_ERR_UNSUPPORTED, "at most 2^24 tokens, 2^24 columns and 2^20 hidden values");
+    if (d.tokens > (1 << 20) || d.vocab > (1 << 24) || d.hidden > (1 << 20))
+        return fail(GEMM_ERR_UNSUPPORTED, "at most 2^20 tokens, 2^24 columns and 2^20 hidden values");
     if (!is_16bit(d.x_type))
         return fail(GEMM_ERR_UNSUPPORTED, "X must be f16 or bf16");
     if (!is_float(d.dx_type) || !is_float(d.dw_type))
@@ -225,26 +226,69 @@ static int64_t tiles(int t, int64_t m, int64_t n)
     return ceil_div(m, xent_edge(t)) * ceil_div(n, xent_edge(t));
 }
 
+// What a product of m x n outputs and a sum of k takes in a tile's rounds of
+// workgroups, us: a 64-value step of the sum and the rest of a tile's way (its
+// first operands, its epilogue), with one workgroup of 256 x 256 on a compute
+// unit and two of the others.  Fitted on the measured kernels; within some 20 %
+// of them, and in their order: 265 tokens, 19890 x 840, dW 32 / 31 / 54 us for
+// 256 / 128 / 64 (measured 38, 31, 44); 3 tokens, 172148 x 72, 31 / 21 (41, 25);
+// 137, 32408 x 7096, 186 / 243 (220, 249); logits of 260, 58186 x 88, 24 / 23 /
+// 43 (26, 24, 35); 442, 90142 x 456, 62 / 79 (63, 77); 556, 1379 x 7920, 189 /
+// 118 / 54 (129, 72, 38).
+static double tile_time(int t, int64_t m, int64_t n, int64_t k, int64_t parts, int num_cu)
+{
+    static const double step[XT_COUNT] = {0.4, 0.9, 1.45}, rest[XT_COUNT] = {4, 6, 9};
+    const int64_t slots = t == XT_256 ? num_cu : 2 * num_cu;
+    return (double)ceil_div(tiles(t, m, n) * parts, slots) *
+           ((double)ceil_div(ceil_div(k, parts), 64) * step[t] + rest[t]);
+}
+
+static int best_tile(int64_t m, int64_t n, int64_t k, int num_cu)
+{
+    int best = XT_64;
+    for (int t = XT_128; t < XT_COUNT; ++t)
+        if (tile_time(t, m, n, k, 1, num_cu) < tile_time(best, m, n, k, 1, num_cu))
+            best = t;
+    return best;
+}
+
 // Tile of the logits' product of `n` columns.
-static int choose_logits(int64_t tokens, int64_t n, int num_cu)
+static int choose_logits(int64_t tokens, int64_t n, int64_t hp, int num_cu)
 {
-    if (tokens <= 64)
-        return XT_64;
-    if (tokens <= 128 || tiles(XT_256, tokens, n) < num_cu)
-        return tiles(XT_128, tokens, n) < num_cu ? XT_64 : XT_128;
-    return XT_256;
+    if (tokens <= XENT_STREAM_ROWS)
+        return XT_STREAM;
+    return tokens <= 64 ? XT_64 : best_tile(tokens, n, hp, num_cu);
 }
 
-static int choose_dw(int64_t piece, int64_t hp, int num_cu)
+// Parts of dX's sum over `cols` columns that any number of rows may choose:
+// 1024 columns each at least, 128 (which k_xent_out adds up) and four rounds of
+// workgroups at most.
+static XentSplits dx_split(int tile, int64_t hp, int64_t cols, int num_cu)
 {
-    if (tiles(XT_256, piece, hp) >= num_cu)
-        return XT_256;
-    return tiles(XT_128, piece, hp) >= num_cu ? XT_128 : XT_64;
+    const int e = xent_edge(tile), slots = tile == XT_256 ? num_cu : 2 * num_cu;
+    const int tiles_n = (int)ceil_div(hp, e);
+    int64_t most = ceil_div(cols, 1024);
+    most = most < 4 * slots / tiles_n ? most : 4 * slots / tiles_n;
+    most = most < 128 ? most : 128;
+    return {e, tiles_n, (int)cols, slots, most < 1 ? 1 : (int)most, 0, num_cu};
 }
 
-static int choose_dx(int64_t tokens, int64_t hp)
+static int choose_dx(int64_t tokens, int64_t hp, int64_t cols, int num_cu)
 {
-    return tokens <= 64 || hp <= 64 ? XT_64 : tokens <= 128 || hp <= 128 ? XT_128 : XT_256;
+    int best = XT_64;
+    double least = 0;
+    for (int t = XT_64; t < XT_COUNT; ++t) {
+        const XentSplits x = dx_split(t, hp, cols, num_cu);
+        const int s = xent_splits((int)tokens, x.edge, x.tiles_n, x.cols, x.slots, x.most);
+        // (each part is written and read again, at 5 TB/s)
+        const double us =
+            tile_time(t, tokens, hp, cols, s, num_cu) + 8e-6 / 5 * (double)(s * tokens * hp);
+        if (t == XT_64 || us < least) {
+            best = t;
+            least = us;
+        }
+    }
+    return best;
 }
 
 static void choose(gemm_xent_plan_t &p, int num_cu)
@@ -254,34 +298,47 @@ static void choose(gemm_xent_plan_t &p, int num_cu)
     // the main loop addresses 256 rows of W with 32-bit offsets
     p.copy = d.hidden % 8 != 0 || d.ldw % 8 != 0 || d.ldw >= (1 << 21) || d.unaligned;
     // G of a piece: 512 MB, W's copy too
-    int64_t most = ((int64_t)1 << 28) / (d.tokens > 0 ? d.tokens : 1);
-    if (p.copy && most > ((int64_t)1 << 28) / p.hp)
-        most = ((int64_t)1 << 28) / p.hp;
-    if (most > (1 << 20))
-        most = 1 << 20;
-    most = most < 2048 ? 2048 : most / 256 * 256;
+    int64_t width = ((int64_t)1 << 28) / (d.tokens > 0 ? d.tokens : 1);
+    if (p.copy && width > ((int64_t)1 << 28) / p.hp)
+        width = ((int64_t)1 << 28) / p.hp;
+    if (width > (1 << 20))
+        width = 1 << 20;
+    width = width < 2048 ? 2048 : width / 256 * 256;
     if (d.piece > 0)
-        most = d.piece > (1 << 20) ? 1 << 20 : ceil_div(d.piece, 256) * 256;
-    const int64_t n = ceil_div(d.vocab, most);
+        width = d.piece > (1 << 20) ? 1 << 20 : ceil_div(d.piece, 256) * 256;
+    const int64_t n = ceil_div(d.vocab, width);
     p.piece = ceil_div(ceil_div(d.vocab, n), 256) * 256;
     const int64_t cols = d.vocab < p.piece ? d.vocab : p.piece;
-    p.stats = choose_logits(d.tokens, p.copy ? cols : d.vocab, num_cu);
-    p.g = choose_logits(d.tokens, cols, num_cu);
-    p.dw = choose_dw(cols, p.hp, num_cu);
-    p.dx = choose_dx(d.tokens, p.hp);
+    p.stats = choose_logits(d.tokens, p.copy ? cols : d.vocab, p.hp, num_cu);
+    p.g = choose_logits(d.tokens, cols, p.hp, num_cu);
+    p.dw = best_tile(cols, p.hp, d.tokens, num_cu);
+    p.dx = choose_dx(d.tokens, p.hp, cols, num_cu);
     if (const char *force = getenv("STGEMM_FORCE_KERNEL")) {
         static const char *const names[XT_COUNT] = {"tiled64", "tiled128", "tiled256"};
         for (int t = 0; t < XT_COUNT; ++t)
             if (strcmp(force, names[t]) == 0)
                 p.stats = p.g = p.dw = p.dx = t;
     }
-    // dX's sums run over the piece's columns: cut where its tiles would leave
-    // compute units idle, 1024 columns at least
-    const int64_t t = tiles(p.dx, d.tokens > 0 ? d.tokens : 1, p.hp);
-    int64_t s = t >= num_cu ? 1 : num_cu / t;
-    if (s > ceil_div(cols, 1024))
-        s = ceil_div(cols, 1024);
-    p.dx_splits = s < 1 ? 1 : s;
+    // dX's sums run over the piece's columns, cut where its tiles would leave
+    // compute units idle.  The kernels choose by the rows that have a target;
+    // here every number of them needs room.
+    p.split = dx_split(p.dx, p.hp, cols, num_cu);
+    const XentSplits &x = p.split;
+    const int e = x.edge;
+    p.acc = 0;
+    for (int64_t n = 0; n < d.tokens;) {
+        n = n + e < d.tokens ? n + e : d.tokens;
+        const int s = xent_splits((int)n, e, x.tiles_n, x.cols, x.slots, x.most);
+        const int wgs = (int)ceil_div(n, e) * x.tiles_n * s;
+        p.acc = s * n * p.hp > p.acc ? s * n * p.hp : p.acc;
+        p.split.wgs = wgs > p.split.wgs ? wgs : p.split.wgs;
+    }
+}
+
+// Maxima and sums per row that the statistics of n columns leave.
+static int64_t stats_parts(const gemm_xent_plan_t &p, int64_t n)
+{
+    return p.stats == XT_STREAM ? xent_streams(n, p.split.num_cu) : ceil_div(n, xent_edge(p.stats));
 }
 
 // The workspace of a call: args' pointers into it, its bytes.
@@ -290,7 +347,7 @@ static size_t xent_parts(const gemm_xent_plan_t &p, bool backward, void *workspa
 {
     const gemm_xent_desc_t &d = p.d;
     Parts w{(uint8_t *)workspace};
-    w.take(a.count, 1);
+    w.take(a.count, 2);
     w.take(a.pos, d.tokens);
     w.take(a.map, d.tokens);
     w.take(a.tgt, d.tokens);
@@ -299,15 +356,15 @@ static size_t xent_parts(const gemm_xent_plan_t &p, bool backward, void *workspa
         w.take(a.ca, d.tokens);
         w.take(a.cb, d.tokens);
         w.take(a.cl, d.tokens);
-        a.gmaxes = d.tokens > 0 ? ceil_div(d.tokens, XENT_PREP) : 1;
+        a.gmaxes = d.tokens > 0 ? ceil_div(d.tokens, xent_prep(d.tokens)) : 1;
         w.take(a.gmax, a.gmaxes);
-        w.take(acc, p.dx_splits * d.tokens * p.hp);
+        w.take(acc, p.acc);
         w.take(piece.G, d.tokens * p.piece);
         piece.ldg = p.piece;
     } else {
-        const int64_t e = xent_edge(p.stats), full = d.vocab / p.piece;
-        a.part_tiles = p.copy ? full * ceil_div(p.piece, e) + ceil_div(d.vocab - full * p.piece, e)
-                              : ceil_div(d.vocab, e);
+        const int64_t full = d.vocab / p.piece;
+        a.part_tiles = p.copy ? full * stats_parts(p, p.piece) + stats_parts(p, d.vocab - full * p.piece)
+                              : stats_parts(p, d.vocab);
         w.take(a.zt, d.tokens);
         w.take(a.part, a.part_tiles * d.tokens * 2);
     }
@@ -332,9 +389,10 @@ gemm_status_t gemm_xent_plan(const gemm_xent_desc_t *desc, gemm_xent_plan_t **ou
     normalise(p->d);
     p->device = dev;
     choose(*p, di.num_cu);
-    snprintf(p->name, sizeof p->name, "xent_%s_stats%d_g%d_dx%dx%lld_dw%d%s",
-             p->d.x_type == GEMM_BF16 ? "bf16" : "f16", xent_edge(p->stats), xent_edge(p->g),
-             xent_edge(p->dx), (long long)p->dx_splits, xent_edge(p->dw), p->copy ? "_copy" : "");
+    auto logits = [](int t) { return t == XT_STREAM ? XENT_STREAM_ROWS : xent_edge(t); };
+    snprintf(p->name, sizeof p->name, "xent_%s_stats%d_g%d_dx%d_dw%d%s",
+             p->d.x_type == GEMM_BF16 ? "bf16" : "f16", logits(p->stats), logits(p->g),
+             xent_edge(p->dx), xent_edge(p->dw), p->copy ? "_copy" : "");
     static const bool log = [] {
         const char *v = getenv("GEMM_LOG");
         return v && *v && strcmp(v, "0") != 0;
@@ -389,6 +447,8 @@ static void fill_args(XentArgs &a, const gemm_xent_plan_t &p, const void *X, con
     a.X = X;
     a.ldx = p.d.ldx;
     a.targets = targets;
+    a.prep = xent_prep(p.d.tokens);
+    a.dx = p.split;
     a.scale = p.d.scale;
 }
 
@@ -447,13 +507,17 @@ gemm_status_t gemm_xent_forward(const gemm_xent_plan_t *plan, const void *X, con
     fill_args(a, *plan, X, targets);
     a.loss = loss;
     a.lse = lse;
-    LAUNCH(launch_xent_prepare(a, false, s));
+    // (one tile of rows: nothing is gained by skipping some)
+    a.direct = d.tokens <= 64 && d.hidden % 8 == 0 && d.ldx % 8 == 0 && d.ldx < (1 << 21) &&
+               aligned(X, 16);
+    if (!a.direct)
+        LAUNCH(launch_xent_prepare(a, false, s));
     const int64_t step = plan->copy ? plan->piece : d.vocab;
     for (p.v0 = 0; p.v0 < d.vocab; p.v0 += step) {
         p.n = d.vocab - p.v0 < step ? d.vocab - p.v0 : step;
         LAUNCH(take_w(*plan, W, copy, p, s));
         LAUNCH(launch_xent_stats(plan->stats, a, p, s));
-        p.tile0 += ceil_div(p.n, xent_edge(plan->stats));
+        p.tile0 += stats_parts(*plan, p.n);
     }
     return launched(launch_xent_loss(a, s));
 }
@@ -495,10 +559,8 @@ gemm_status_t gemm_xent_backward(const gemm_xent_plan_t *plan, const void *X, co
         LAUNCH(take_w(*plan, W, copy, p, s));
         if (t > 0)
             LAUNCH(launch_xent_g(plan->g, a, p, s));
-        if (dX && t > 0) {
-            const int64_t k = ceil_div(ceil_div(p.n, plan->dx_splits), 64) * 64;
-            LAUNCH(launch_xent_dx(plan->dx, a, p, {acc, (int)plan->dx_splits, k, p.v0 > 0}, s));
-        }
+        if (dX && t > 0)
+            LAUNCH(launch_xent_dx(plan->dx, a, p, {acc, p.v0 > 0}, s));
         if (dW) {
             uint8_t *w = (uint8_t *)dW + p.v0 * d.lddw * wb;
             // the vector epilogue addresses 257 rows of dW with 32-bit offsets
@@ -510,7 +572,7 @@ gemm_status_t gemm_xent_backward(const gemm_xent_plan_t *plan, const void *X, co
         }
     }
     if (dX && t > 0)
-        LAUNCH(launch_xent_out(a, {acc, (int)plan->dx_splits, dX, d.lddx, out_kind(d.dx_type)}, s));
+        LAUNCH(launch_xent_out(a, {acc, dX, d.lddx, out_kind(d.dx_type)}, s));
     return ok();
 }
 

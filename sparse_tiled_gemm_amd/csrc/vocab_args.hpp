@@ -49,22 +49,66 @@ hipError_t launch_embed_backward(const EmbedArgs &a, hipStream_t s);
 // ---------------------------------------------------------------- linear cross entropy
 
 // Workgroup tiles of a product.
-enum XentTile { XT_64 = 0, XT_128, XT_256, XT_COUNT };
+enum XentTile {
+    XT_64 = 0,
+    XT_128,
+    XT_256,
+    XT_COUNT,
+    XT_STREAM = XT_COUNT // the logits of up to 16 rows: no tiles, columns in turn
+};
 inline int xent_edge(int t) { return t == XT_256 ? 256 : t == XT_128 ? 128 : 64; }
 
-// tokens of a workgroup of the preparing kernel
-constexpr int XENT_PREP = 32;
+// tokens of a step of the preparing kernel, and of one of its workgroups: more
+// where looking through all targets before them would count
+constexpr int XENT_STEP = 32;
+inline int xent_prep(int64_t tokens) { return tokens <= 32768 ? XENT_STEP : 8 * XENT_STEP; }
+
+// Parts that dX's sum over `cols` columns of a piece is cut into, for n rows of
+// tiles of `edge` and tiles_n columns of them: those that fill 1 to 4 rounds of
+// the chip's `slots` workgroups, or one, whichever is cheapest, a tile's way
+// costing some 600 columns besides.  Sizes are below 2^21, tiles below 2^22.
+inline __host__ __device__ int xent_splits(int n, int edge, int tiles_n, int cols, int slots, int most)
+{
+    const int tiles = (n + edge - 1) / edge * tiles_n;
+    int best = 1, cost = INT32_MAX;
+    for (int r = 0; r <= 4; ++r) {
+        int s = r == 0 || tiles == 0 ? 1 : slots * r / tiles;
+        s = s < 1 ? 1 : s > most ? most : s;
+        const float c = (float)((tiles * s + slots - 1) / slots) * (float)((cols + s - 1) / s + 600);
+        if (c < (float)cost) {
+            cost = c < 2e9f ? (int)c : INT32_MAX;
+            best = s;
+        }
+    }
+    return best;
+}
+struct XentSplits {
+    int edge, tiles_n, cols, slots, most;
+    int wgs; // workgroups at most: tiles times parts
+    int num_cu;
+};
+// Workgroups of the streaming kernel, four waves with 16 columns at a time
+// each: two to a compute unit.
+constexpr int XENT_STREAM_ROWS = 16;
+inline int64_t xent_streams(int64_t n, int num_cu)
+{
+    const int64_t g = (n + 63) / 64;
+    return g < 2 * num_cu ? g : 2 * num_cu;
+}
 
 struct XentArgs {
     int64_t tokens, vocab, hidden, hp; // hp: hidden in whole 16-byte chunks
     int id8, bf16;
     const void *X, *targets;
     int64_t ldx;
+    int prep;   // tokens per workgroup of the preparing kernel
+    int direct; // forward, few tokens: X is read where it lies, every token is a row
+    XentSplits dx;
     float scale;
     const float *lse_in, *dloss, *dlse; // backward
     float *loss, *lse;                  // forward
     // the workspace: rows are the tokens with a target, in order
-    int32_t *count;       // rows
+    int32_t *count;       // rows, and (backward) parts of dX's sum
     int32_t *pos, *map;   // row of a token (-1: none), token of a row
     int32_t *tgt;         // target of a row
     float *ca, *cb, *cl;  // of a row: dloss + dlse, dloss, lse / ln 2
@@ -95,10 +139,8 @@ struct XentCopy {
 };
 
 struct XentDx { // acc[split] (+)= G W
-    float *acc;  // [splits][tokens][hp]
-    int splits;
-    int64_t k_split; // columns of the piece per split, a multiple of 64
-    int add;         // add to what acc holds
+    float *acc; // [splits][rows][hp]
+    int add;    // add to what acc holds
 };
 struct XentDw {
     void *dW; // the piece's first row
@@ -107,7 +149,6 @@ struct XentDw {
 };
 struct XentOut { // dX = the sum of acc, scaled, by token
     const float *acc;
-    int splits;
     void *dX;
     int64_t ldd;
     int d_kind;

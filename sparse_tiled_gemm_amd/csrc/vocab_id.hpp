@@ -11,8 +11,9 @@ namespace stg {
 __device__ STG_AI inline int vocab_id(const void *ids, int id8, int64_t vocab, int64_t t)
 {
     const int32_t *p = (const int32_t *)ids + (t << id8);
-    const int32_t lo = p[0], hi = p[id8] & -id8;
-    return hi == 0 && (uint32_t)lo < (uint32_t)vocab ? lo : -1;
+    int32_t lo = p[0], hi = p[id8];
+    asm("" : "+v"(lo), "+v"(hi)); // (neither load waits for the other's value)
+    return ((hi & -id8) == 0) & ((uint32_t)lo < (uint32_t)vocab) ? lo : -1;
 }
 
 } // namespace stg

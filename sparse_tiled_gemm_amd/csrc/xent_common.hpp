@@ -12,17 +12,40 @@ __device__ STG_AI inline int xent_target(const XentArgs &a, int64_t t)
     return vocab_id(a.targets, a.id8, a.vocab, t);
 }
 
+// Rows, and a row's target.
+__device__ STG_AI inline int xent_rows(const XentArgs &a)
+{
+    return a.direct ? (int)a.tokens : __builtin_amdgcn_readfirstlane(*a.count);
+}
+__device__ STG_AI inline int xent_row_target(const XentArgs &a, int64_t row)
+{
+    return a.direct ? xent_target(a, row) : a.tgt[row];
+}
+
 // The logits' gradient enters its products as a 16-bit value relative to the
 // call's largest coefficient: |G| <= 2 F with F = 1, or 2^14 for fp16, whose
 // normal values then begin at 2^-28 of that coefficient (a probability of 4e-9)
 // instead of 2^-14.
 __device__ STG_AI inline float xent_unit(const XentArgs &a) { return a.bf16 ? 1.0f : 16384.0f; }
 
-// The largest coefficient of the call; every wave computes it.
-__device__ STG_AI inline float xent_gmax(const XentArgs &a, int lane)
+// The largest coefficient of the call; every wave computes it, the first 256
+// values from loads that were begun earlier.
+struct Gmax {
+    float v[4];
+};
+__device__ STG_AI inline Gmax load_gmax(const XentArgs &a, int lane)
 {
-    float g = 0.0f;
-    for (int64_t i = lane; i < a.gmaxes; i += 64)
+    Gmax g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) // (past the end: the last one again)
+        g.v[i] = a.gmax[min((int64_t)lane + 64 * i, a.gmaxes - 1)];
+    return g;
+}
+__device__ STG_AI inline float xent_gmax(const XentArgs &a, const Gmax &first, int lane)
+{
+    float g = __builtin_fmaxf(__builtin_fmaxf(first.v[0], first.v[1]),
+                              __builtin_fmaxf(first.v[2], first.v[3]));
+    for (int64_t i = lane + 256; i < a.gmaxes; i += 64)
         g = __builtin_fmaxf(g, a.gmax[i]);
 #pragma unroll
     for (int d = 32; d; d >>= 1)
@@ -31,9 +54,9 @@ __device__ STG_AI inline float xent_gmax(const XentArgs &a, int lane)
 }
 
 // What a product of G is multiplied by.
-__device__ STG_AI inline float xent_factor(const XentArgs &a, int lane)
+__device__ STG_AI inline float xent_factor(const XentArgs &a, const Gmax &first, int lane)
 {
-    return xent_gmax(a, lane) / xent_unit(a) * a.scale;
+    return xent_gmax(a, first, lane) / xent_unit(a) * a.scale;
 }
 
 } // namespace stg

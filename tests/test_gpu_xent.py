@@ -99,7 +99,8 @@ def run(tokens, vocab, hidden, dtype, dx="f32", dw="f32", scale=1.0, ignore=0.2,
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("tokens,vocab,hidden", [
     (1, 1, 8), (1, 1000, 64), (1, 5000, 128), (5, 63, 72), (64, 513, 64), (65, 300, 136), (130, 1111, 264),
-    (257, 777, 200), (300, 2048, 64), (513, 1025, 128)])
+    (257, 777, 200), (300, 2048, 64), (513, 1025, 128), (2, 70001, 40), (16, 40000, 200),
+    (17, 3000, 136)])
 def test_sizes(dtype, tokens, vocab, hidden):
     run(tokens, vocab, hidden, dtype)
 
@@ -116,7 +117,8 @@ def test_every_tile(monkeypatch, tile, dtype, tokens, vocab, hidden, piece):
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("tokens,vocab,hidden,pad,off,piece", [
     (33, 501, 1, 0, 0, 0), (150, 700, 77, 0, 0, 256), (70, 300, 63, 2, 1, 0), (40, 300, 64, 0, 3, 256),
-    (300, 600, 129, 7, 5, 256), (90, 400, 64, 8, 8, 0), (90, 400, 64, 3, 0, 0)])
+    (300, 600, 129, 7, 5, 256), (90, 400, 64, 8, 8, 0), (90, 400, 64, 3, 0, 0), (9, 1000, 130, 0, 0, 256),
+    (16, 900, 264, 8, 8, 512)])
 def test_odd_widths_and_strides(dtype, tokens, vocab, hidden, pad, off, piece):
     run(tokens, vocab, hidden, dtype, dx=dtype, dw="f32", pad=pad, off=off, piece=piece, id_bytes=4)
 
