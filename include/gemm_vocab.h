@@ -90,8 +90,9 @@ gemm_status_t gemm_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, i
  * the products are summed in fp32 and rounded once.
  *
  * x_type GEMM_F16 or GEMM_BF16; dx_type and dw_type GEMM_F32, GEMM_F16 or
- * GEMM_BF16.  1 <= hidden <= 2^20, 1 <= vocab <= 2^24, tokens <= 2^20.
- * Where hidden, ldx or ldw are no multiples of 8, or W is not 16-byte aligned
+ * GEMM_BF16.  1 <= hidden <= 2^15, 1 <= vocab <= 2^24, tokens <= 2^20,
+ * and at most 2^36 logits.
+ * Where hidden or ldw is no multiple of 8, or W is not 16-byte aligned
  * (`unaligned` = 1 makes room for that; GEMM_ERR_MISALIGNED without it), W is
  * copied to the workspace piece by piece. */
 typedef struct {

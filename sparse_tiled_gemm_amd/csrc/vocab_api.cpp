@@ -209,8 +209,8 @@ gemm_status_t gemm_xent_validate_desc(const gemm_xent_desc_t *desc)
     for (int64_t ld : {d.ldx, d.ldw, d.lddx, d.lddw})
         if (ld > MAX_ELEMS || smul(d.tokens > d.vocab ? d.tokens : d.vocab, ld) > MAX_ELEMS)
             return fail(GEMM_ERR_INVALID_VALUE, "a matrix spans more than 2^40 elements");
-    if (d.tokens > (1 << 20) || d.vocab > (1 << 24) || d.hidden > (1 << 20))
-        return fail(GEMM_ERR_UNSUPPORTED, "at most 2^20 tokens, 2^24 columns and 2^20 hidden values");
+    if (d.tokens > (1 << 20) || d.vocab > (1 << 24) || d.hidden > (1 << 15))
+        return fail(GEMM_ERR_UNSUPPORTED, "at most 2^20 tokens, 2^24 columns and 2^15 hidden values");
     if (!is_16bit(d.x_type))
         return fail(GEMM_ERR_UNSUPPORTED, "X must be f16 or bf16");
     if (!is_float(d.dx_type) || !is_float(d.dw_type))

@@ -106,7 +106,7 @@ def desc(**kw):
     (dict(ldw=-1), INVALID), (dict(lddx=1), INVALID), (dict(lddw=1 << 41), INVALID),
     (dict(piece=-1), INVALID), (dict(x_type="f32"), UNSUPPORTED), (dict(dx_type="s32"), UNSUPPORTED),
     (dict(dw_type="e5m2"), UNSUPPORTED), (dict(tokens=(1 << 20) + 1), UNSUPPORTED),
-    (dict(vocab=(1 << 24) + 1), UNSUPPORTED), (dict(hidden=(1 << 20) + 1), UNSUPPORTED),
+    (dict(vocab=(1 << 24) + 1), UNSUPPORTED), (dict(hidden=(1 << 15) + 1), UNSUPPORTED),
     (dict(tokens=1 << 20, vocab=1 << 24, hidden=8), UNSUPPORTED),
 ])
 def test_xent_desc(change, status):
