@@ -87,7 +87,8 @@ gemm_status_t gemm_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, i
  * G enters both products as a value of x_type relative to the largest |dloss|
  * and |dloss + dlse| of the call (fp16 with 14 more binades above the
  * smallest), so that gradients far below that type's range keep their bits;
- * the products are summed in fp32 and rounded once.
+ * the products are summed in fp32 and rounded once.  An infinity or NaN among a
+ * token's values reaches its row of dX and dW.
  *
  * x_type GEMM_F16 or GEMM_BF16; dx_type and dw_type GEMM_F32, GEMM_F16 or
  * GEMM_BF16.  1 <= hidden <= 2^15, 1 <= vocab <= 2^24, tokens <= 2^20,

@@ -6,6 +6,13 @@
 
 namespace stg {
 
+// |x|, 0 for an infinity or NaN
+__device__ STG_AI inline float finite_abs(float x)
+{
+    x = __builtin_fabsf(x);
+    return x <= 3.402823466e38f ? x : 0.0f;
+}
+
 // Rows, targets and coefficients of a.prep tokens, and 512 columns
 // (blockIdx.y) of their rows of X.  A workgroup counts the targets before its
 // tokens by itself, so that one launch does; what it needs of its own tokens
@@ -74,7 +81,7 @@ __global__ __launch_bounds__(256) void k_xent_prepare(XentArgs a)
                     a.ca[row] = ca;
                     a.cb[row] = cb;
                     a.cl[row] = cl * LOG2E;
-                    g = __builtin_fmaxf(g, __builtin_fmaxf(__builtin_fabsf(ca), __builtin_fabsf(cb)));
+                    g = __builtin_fmaxf(g, __builtin_fmaxf(finite_abs(ca), finite_abs(cb)));
                 }
             } else if (in && !BACKWARD) {
                 a.lse[t] = 0.0f;
@@ -87,7 +94,7 @@ __global__ __launch_bounds__(256) void k_xent_prepare(XentArgs a)
             const int64_t to = __shfl(row, wave * R + i);
             if (to < 0 || c >= a.hp)
                 continue;
-            *(u4_t *)(a.Xc + to * a.hp + c) =
+            *(u4_t *)(a.Xc + to * a.ldc + c) =
                 full ? x[i] : load8((const uint16_t *)a.X + (t0 + wave * R + i) * a.ldx + c, nc);
         }
     }
@@ -117,7 +124,7 @@ __global__ __launch_bounds__(256) void k_xent_copy(XentCopy c)
     for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < c.n; r += (int64_t)gridDim.x * 4)
         for (int i = lane; i < pieces; i += 64) {
             const int n = (int)min((int64_t)8, c.hidden - i * 8);
-            *(u4_t *)(c.out + r * c.hp + i * 8) = load8(c.W + r * c.ldw + i * 8, n);
+            *(u4_t *)(c.out + r * c.ldo + i * 8) = load8(c.W + r * c.ldw + i * 8, n);
         }
 }
 

@@ -53,7 +53,7 @@ __device__ STG_AI inline GroupedArgs dw_args(const XentArgs &a, const XentPiece 
     g.A = p.G;
     g.lda = p.ldg;
     g.B = a.Xc;
-    g.ldb = a.hp;
+    g.ldb = a.ldc;
     return g;
 }
 __device__ STG_AI inline EpiArgs dw_epilogue(const XentArgs &a, const XentPiece &p, const XentDw &d)

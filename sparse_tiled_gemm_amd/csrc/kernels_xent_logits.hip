@@ -154,9 +154,9 @@ __device__ STG_AI inline void tile_g(const XentArgs &a, const XentPiece &p, int6
     const int tid = threadIdx.x, l16 = lane & 15, q = lane >> 4;
     const int rb = wave / S::GN * S::WM, cb = wave % S::GN * S::WN;
     const float gmax = xent_gmax(a, row.gmax, lane), f = xent_unit(a);
-    if (tid < S::BM) { // (gmax 0: every coefficient is)
-        rows[tid] = gmax != 0.0f ? row.ca / gmax * f : 0.0f;
-        rows[S::BM + tid] = gmax != 0.0f ? row.cb / gmax * f : 0.0f;
+    if (tid < S::BM) {
+        rows[tid] = row.ca / gmax * f;
+        rows[S::BM + tid] = row.cb / gmax * f;
         rows[2 * S::BM + tid] = row.cl;
         ((int *)rows)[3 * S::BM + tid] = row.tgt;
     }
@@ -205,7 +205,7 @@ __device__ STG_AI inline GroupedArgs logits_args(const XentArgs &a, const XentPi
     GroupedArgs g{};
     g.N = p.n;
     g.A = a.direct ? a.X : a.Xc;
-    g.lda = a.direct ? a.ldx : a.hp;
+    g.lda = a.direct ? a.ldx : a.ldc;
     g.B = p.W;
     g.ldb = p.ldw;
     return g;
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p,
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = gridDim.x * 4;
     const int n = xent_rows(a), KT = (int)((a.hp + 127) / 128);
-    const int64_t kb = a.hp * 2, ldw = p.ldw * 2, lda = (a.direct ? a.ldx : a.hp) * 2;
+    const int64_t kb = a.hp * 2, ldw = p.ldw * 2, lda = (a.direct ? a.ldx : a.ldc) * 2;
     const __amdgpu_buffer_rsrc_t ra =
         tile_rsrc(a.direct ? a.X : a.Xc, n > 0 ? (n - 1) * lda + kb : 0);
     auto buf = [&](auto slot) STG_AI {
@@ -351,10 +351,10 @@ __global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p,
         tgt[r] = 4 * q + r < n ? tgt[r] : -1;
         m[r] = -INFINITY;
         s[r] = 0.0f;
-        if constexpr (GRAD) { // (gmax 0: every coefficient is)
+        if constexpr (GRAD) {
             const float f = xent_unit(a);
-            ca[r] = gmax != 0.0f ? __shfl(row.ca, 4 * q + r) / gmax * f : 0.0f;
-            cb[r] = gmax != 0.0f ? __shfl(row.cb, 4 * q + r) / gmax * f : 0.0f;
+            ca[r] = __shfl(row.ca, 4 * q + r) / gmax * f;
+            cb[r] = __shfl(row.cb, 4 * q + r) / gmax * f;
             cl[r] = __shfl(row.cl, 4 * q + r);
         }
     }

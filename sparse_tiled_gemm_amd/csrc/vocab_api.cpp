@@ -351,7 +351,8 @@ static size_t xent_parts(const gemm_xent_plan_t &p, bool backward, void *workspa
     w.take(a.pos, d.tokens);
     w.take(a.map, d.tokens);
     w.take(a.tgt, d.tokens);
-    w.take(a.Xc, d.tokens * p.hp);
+    a.ldc = xent_pitch(d.hidden);
+    w.take(a.Xc, d.tokens * a.ldc);
     if (backward) {
         w.take(a.ca, d.tokens);
         w.take(a.cb, d.tokens);
@@ -369,7 +370,7 @@ static size_t xent_parts(const gemm_xent_plan_t &p, bool backward, void *workspa
         w.take(a.part, a.part_tiles * d.tokens * 2);
     }
     if (p.copy)
-        w.take(copy, (d.vocab < p.piece ? d.vocab : p.piece) * p.hp);
+        w.take(copy, (d.vocab < p.piece ? d.vocab : p.piece) * a.ldc);
     return w.at;
 }
 
@@ -471,8 +472,8 @@ static hipError_t take_w(const gemm_xent_plan_t &p, const void *W, uint16_t *cop
 {
     const uint16_t *w = (const uint16_t *)W + piece.v0 * p.d.ldw;
     piece.W = p.copy ? copy : w;
-    piece.ldw = p.copy ? p.hp : p.d.ldw;
-    return p.copy ? launch_xent_copy({w, p.d.ldw, piece.n, p.d.hidden, p.hp, copy}, s) : hipSuccess;
+    piece.ldw = p.copy ? xent_pitch(p.d.hidden) : p.d.ldw;
+    return p.copy ? launch_xent_copy({w, p.d.ldw, piece.n, p.d.hidden, p.hp, copy, piece.ldw}, s) : hipSuccess;
 }
 
 #define LAUNCH(x)                                 \

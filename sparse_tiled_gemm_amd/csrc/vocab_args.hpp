@@ -114,7 +114,8 @@ struct XentArgs {
     float *ca, *cb, *cl;  // of a row: dloss + dlse, dloss, lse / ln 2
     float *gmax;          // largest |ca|, |cb| of each workgroup's tokens
     int64_t gmaxes;
-    uint16_t *Xc;         // rows x hp
+    uint16_t *Xc;         // rows x hp, ldc apart: whole cache lines (xent_pitch)
+    int64_t ldc;
     float *zt;            // target's logit of a row
     float *part;          // [tile column][row] maximum and sum
     int64_t part_tiles;
@@ -130,12 +131,17 @@ struct XentPiece {
     int64_t ldg;
 };
 
+// Elements between the rows of X and of a piece of W in the workspace: rows on
+// cache lines (those of 1416 values, 22.1 lines, cost the products 15 %).
+inline int64_t xent_pitch(int64_t hidden) { return (hidden + 63) / 64 * 64; }
+
 // W's rows v0 .. v0 + n - 1 (hidden values each) to out (hp each, zeros at
-// the end)
+// the end, ldo apart)
 struct XentCopy {
     const uint16_t *W;
     int64_t ldw, n, hidden, hp;
     uint16_t *out;
+    int64_t ldo;
 };
 
 struct XentDx { // acc[split] (+)= G W

@@ -28,8 +28,9 @@ __device__ STG_AI inline int xent_row_target(const XentArgs &a, int64_t row)
 // instead of 2^-14.
 __device__ STG_AI inline float xent_unit(const XentArgs &a) { return a.bf16 ? 1.0f : 16384.0f; }
 
-// The largest coefficient of the call; every wave computes it, the first 256
-// values from loads that were begun earlier.
+// The largest finite coefficient of the call, 1 if there is none but zeros
+// (an infinity or NaN stays what it is in its own row); every wave computes it,
+// the first 256 values from loads that were begun earlier.
 struct Gmax {
     float v[4];
 };
@@ -50,7 +51,7 @@ __device__ STG_AI inline float xent_gmax(const XentArgs &a, const Gmax &first, i
 #pragma unroll
     for (int d = 32; d; d >>= 1)
         g = __builtin_fmaxf(g, __shfl_xor(g, d));
-    return g;
+    return g > 0.0f ? g : 1.0f;
 }
 
 // What a product of G is multiplied by.

@@ -57,7 +57,7 @@ static void check_args(const XentArgs &a, bool backward)
     EXPECT(a.tokens >= 0 && a.tokens <= (1 << 20) && a.hp % 8 == 0 && a.hp >= a.hidden);
     EXPECT(a.prep > 0 && a.prep % XENT_STEP == 0);
     EXPECT(inside(a.count, 2, 4) && inside(a.pos, a.tokens, 4) && inside(a.map, a.tokens, 4));
-    EXPECT(inside(a.tgt, a.tokens, 4) && inside(a.Xc, a.tokens * a.hp, 2));
+    EXPECT(inside(a.tgt, a.tokens, 4) && a.ldc >= a.hp && inside(a.Xc, a.tokens * a.ldc, 2));
     if (backward) {
         EXPECT(inside(a.ca, a.tokens, 4) && inside(a.cb, a.tokens, 4) && inside(a.cl, a.tokens, 4));
         EXPECT(a.gmaxes >= 1 && a.gmaxes * a.prep >= a.tokens && inside(a.gmax, a.gmaxes, 4));
@@ -87,7 +87,7 @@ hipError_t launch_xent_prepare(const XentArgs &a, bool backward, hipStream_t)
 }
 hipError_t launch_xent_copy(const XentCopy &c, hipStream_t)
 {
-    EXPECT(c.W && c.n > 0 && c.ldw >= c.hidden && inside(c.out, c.n * c.hp, 2));
+    EXPECT(c.W && c.n > 0 && c.ldw >= c.hidden && c.ldo >= c.hp && inside(c.out, c.n * c.ldo, 2));
     return hipSuccess;
 }
 hipError_t launch_xent_stats(int tile, const XentArgs &a, const XentPiece &p, hipStream_t)

@@ -38,7 +38,8 @@ def outputs(tokens, cols, dtype, ld):
 
 
 def run(tokens, vocab, hidden, dtype, dx="f32", dw="f32", scale=1.0, ignore=0.2, id_bytes=8, pad=0,
-        off=0, piece=0, accumulate=False, dlse=True, data=None, gscale=1.0, spread=1.0):
+        off=0, piece=0, accumulate=False, dlse=True, data=None, gscale=1.0, spread=1.0,
+        unaligned=False):
     say("xent", tokens, vocab, hidden, dtype, dx, dw, scale, ignore, pad, off, piece, accumulate)
     X, W, y = data or make(tokens, vocab, hidden, dtype, ignore, spread=spread)
     gen = torch.Generator().manual_seed(9)
@@ -46,7 +47,7 @@ def run(tokens, vocab, hidden, dtype, dx="f32", dw="f32", scale=1.0, ignore=0.2,
     yd = y.cuda() if id_bytes == 8 else y.to(torch.int32).cuda()
     plan = G.gemm_xent_plan(G.make_xent_desc(
         tokens, vocab, hidden, dtype, dx, dw, scale=scale, accumulate=accumulate, id_bytes=id_bytes,
-        unaligned=off % 8 != 0, ldx=hidden + pad, ldw=hidden + pad, lddx=hidden + pad,
+        unaligned=unaligned or off % 8 != 0, ldx=hidden + pad, ldw=hidden + pad, lddx=hidden + pad,
         lddw=hidden + 2 * pad, piece=piece))
     nf, nb = G.gemm_xent_workspace(plan)
     ws = [torch.full((n + 64,), 0xFF, dtype=torch.uint8, device="cuda") for n in (nf, nb)]
@@ -153,6 +154,33 @@ def test_tokens_without_target(tokens, ignore):
 @pytest.mark.parametrize("piece", [1, 256, 300, 512, 1024, 1 << 20])
 def test_pieces(piece):
     run(140, 1500, 80, "f16", dx="f16", dw="f16", piece=piece)
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 100])
+def test_copied_weights_beside_rows_that_are_read_where_they_lie(tokens):
+    run(tokens, 700, 64, "bf16", unaligned=True, piece=256)
+
+
+@pytest.mark.parametrize("tokens", [4, 100])
+def test_an_infinite_coefficient_stays_in_its_row(tokens):
+    """One token's dloss overflowed: its row of dX and dW say so, the other rows
+    of dX keep their values."""
+    vocab, hidden = 300, 64
+    X, W, y = make(tokens, vocab, hidden, "f16", ignore=0.0)
+    plan = G.gemm_xent_plan(G.make_xent_desc(tokens, vocab, hidden, "f16", "f32", "f32", id_bytes=8))
+    ws = torch.empty(max(G.gemm_xent_workspace(plan)), dtype=torch.uint8, device="cuda")
+    ref = Xent(X, W, y, 1.0)
+    lse = ref.lse_rows.float()
+    for bad in (float("inf"), float("nan")):
+        g = torch.full((tokens,), 0.25)
+        g[2] = bad
+        dX, dW = torch.empty(tokens, hidden, device="cuda"), torch.empty(vocab, hidden, device="cuda")
+        G.gemm_xent_backward(plan, X.cuda(), W.cuda(), y.cuda(), lse.cuda(), g.cuda(), None, dX, dW, ws)
+        good = torch.arange(tokens) != 2
+        g[2] = 0.25
+        gX, _, bX, _ = ref.grads(lse, g, None, "f16")
+        assert far(dX[good.cuda()], gX[good], bX[good], "f32") <= 0
+        assert not bool(torch.isfinite(dX[2]).any()) and not bool(torch.isfinite(dW[y[2]]).any())
 
 
 def test_no_dlse():
