@@ -3,8 +3,8 @@
 // The lookup Y[t] = s E[id_t] is one pass of 16-byte pieces; bound by memory.
 //
 // The gradient dE[v] = s sum of dY[t] over the tokens t of row v needs the
-// tokens grouped by row.  Up to EMBED_SMALL tokens one launch does it without
-// a sort: a workgroup per token looks through all ids, leaves if an earlier
+// tokens grouped by row.  Up to EMBED_SMALL tokens one launch (behind one
+// that writes the zeros, if the whole gradient is written) does it without a sort: a workgroup per token looks through all ids, leaves if an earlier
 // token has its id, and sums the rows of the later ones otherwise.  More
 // tokens are sorted in two stable passes, by the low bits of the id (counts
 // and places of chunks, as the routing's sort) and, a workgroup per bin, by
@@ -45,7 +45,7 @@ struct Raw8 {
     u4_t v[elem_bytes(K) / 2];
 };
 
-// FULL: all eight exist; else the first n (0 .. 8), zeros after them.
+// FULL: all eight exist; else the first n (0 .. 7), zeros after them.
 template <int K, bool FULL>
 __device__ STG_AI inline Raw8<K> load_raw(const void *base, int64_t off, int n)
 {
@@ -83,59 +83,69 @@ __device__ STG_AI inline void widen_raw(const Raw8<K> &r, float (&f)[8])
     }
 }
 
-// NT: past the caches.
-template <int K, bool FULL, bool NT = false>
-__device__ STG_AI inline void store_raw(void *base, int64_t off, int n, const float (&f)[8])
-{
-    auto put = [](void *p, u4_t v) STG_AI {
-        if constexpr (NT)
-            __builtin_nontemporal_store(v, &((u4_any_t *)p)->v);
-        else
-            ((u4_any_t *)p)->v = v;
-    };
-    if constexpr (K == OUT_F32) {
-        uint8_t *p = (uint8_t *)base + off * 4;
-        if constexpr (FULL) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                put(p + 16 * i, __builtin_bit_cast(u4_t, f4_t{f[4 * i], f[4 * i + 1], f[4 * i + 2],
-                                                              f[4 * i + 3]}));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < n)
-                    ((float *)p)[e] = f[e];
-        }
-    } else if constexpr (FULL) {
-        put((uint16_t *)base + off, narrow8<K == OUT_BF16>(f));
-    } else {
-        const u4_t v = narrow8<K == OUT_BF16>(f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < n)
-                ((uint16_t *)base)[off + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-    }
-}
-
-// The columns of a lane: c .. c + n - 1 (n 0: none, c then is 0).
+// The columns of a lane: elements e0 .. 7 of the eight from column c on (e0 8:
+// none).  A row's last lane takes the row's last eight columns, of which the
+// first e0 belong to the lane before it, so that every lane loads whole pieces;
+// rows of less than eight columns (FULL false) have one lane with n of them.
 struct Cols {
     int64_t c;
-    int n;
+    int e0, n;
 };
 __device__ STG_AI inline Cols lane_cols(const EmbedArgs &a, int64_t c)
 {
+    if (a.cols < 8)
+        return {0, c == 0 ? 0 : 8, c == 0 ? (int)a.cols : 0};
     const int64_t left = a.cols - c;
-    return {left > 0 ? c : 0, left >= 8 ? 8 : left > 0 ? (int)left : 0};
+    return {min(c, a.cols - 8), left >= 8 ? 0 : left > 0 ? 8 - (int)left : 8, 8};
 }
-// f(FULL): FULL where every lane of the wave that has columns has eight (the
-// others may load from column 0).
 template <class F>
-__device__ STG_AI inline void with_full(const EmbedArgs &a, const Cols &k, F &&f)
+__device__ STG_AI inline void with_full(const EmbedArgs &a, F &&f)
 {
-    if (a.cols >= 8 && __all(k.n == 8 || k.n == 0))
+    if (a.cols >= 8)
         f(std::true_type{});
     else
         f(std::false_type{});
+}
+
+// A lane's columns of the row at element `row`.
+template <int K, bool FULL>
+__device__ STG_AI inline Raw8<K> load_cols(const void *base, int64_t row, const Cols &k)
+{
+    return load_raw<K, FULL>(base, row + k.c, k.n);
+}
+// NT: past the caches.
+template <int K, bool FULL, bool NT = false>
+__device__ STG_AI inline void store_cols(void *base, int64_t row, const Cols &k, const float (&f)[8])
+{
+    uint8_t *const p = (uint8_t *)base + (row + k.c) * elem_bytes(K);
+    auto put = [](void *q, u4_t v) STG_AI {
+        if constexpr (NT)
+            __builtin_nontemporal_store(v, &((u4_any_t *)q)->v);
+        else
+            ((u4_any_t *)q)->v = v;
+    };
+    u4_t v[elem_bytes(K) / 2];
+    if constexpr (K == OUT_F32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            v[i] = __builtin_bit_cast(u4_t, f4_t{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]});
+    } else {
+        v[0] = narrow8<K == OUT_BF16>(f);
+    }
+    if (FULL && k.e0 == 0) {
+#pragma unroll
+        for (int i = 0; i < elem_bytes(K) / 2; ++i)
+            put(p + 16 * i, v[i]);
+    } else if (k.e0 < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e >= k.e0 && (FULL || e < k.n)) {
+                if constexpr (K == OUT_F32)
+                    ((float *)p)[e] = f[e];
+                else
+                    ((uint16_t *)p)[e] = (uint16_t)(v[0][e >> 1] >> (16 * (e & 1)));
+            }
+    }
 }
 
 // Token t's row of the table, -1 for an id that names none.
@@ -154,7 +164,7 @@ __global__ __launch_bounds__(256) void k_embed(EmbedArgs a)
 {
     const Cols k = lane_cols(a, ((int64_t)blockIdx.y * TPR + threadIdx.x % TPR) * 8);
     const int64_t first = ((int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR) * U;
-    with_full(a, k, [&](auto full) STG_AI {
+    with_full(a, [&](auto full) STG_AI {
         constexpr bool FULL = decltype(full)::value;
         for (int64_t t = first; t < a.tokens; t += (int64_t)gridDim.x * (256 / TPR) * U) {
             int id[U];
@@ -166,7 +176,7 @@ __global__ __launch_bounds__(256) void k_embed(EmbedArgs a)
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (a.vocab > 0)
-                    r[u] = load_raw<EK, FULL>(a.in, (id[u] < 0 ? 0 : id[u]) * a.ld_in + k.c, k.n);
+                    r[u] = load_cols<EK, FULL>(a.in, (id[u] < 0 ? 0 : id[u]) * a.ld_in, k);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float f[8] = {};
@@ -176,8 +186,8 @@ __global__ __launch_bounds__(256) void k_embed(EmbedArgs a)
                     for (int e = 0; e < 8; ++e)
                         f[e] *= a.scale;
                 }
-                if (t + u < a.tokens && k.n > 0)
-                    store_raw<YK, FULL, NT>(a.out, (t + u) * a.ld_out + k.c, k.n, f);
+                if (t + u < a.tokens)
+                    store_cols<YK, FULL, NT>(a.out, (t + u) * a.ld_out, k, f);
             }
         }
     });
@@ -201,15 +211,14 @@ __device__ STG_AI inline void put_row(const EmbedArgs &a, int64_t v, const Cols 
         for (int e = 0; e < 8; ++e)
             f[e] += x[e];
     }
-    if (k.n > 0)
-        store_raw<DK, FULL>(a.out, v * a.ld_out + k.c, k.n, f);
+    store_cols<DK, FULL>(a.out, v * a.ld_out, k, f);
 }
 template <int DK, bool FULL>
 __device__ STG_AI inline Raw8<DK> get_row(const EmbedArgs &a, int64_t v, const Cols &k)
 {
     Raw8<DK> d{};
     if (a.accumulate)
-        d = load_raw<DK, FULL>(a.out, v * a.ld_out + k.c, k.n);
+        d = load_cols<DK, FULL>(a.out, v * a.ld_out, k);
     return d;
 }
 
@@ -260,12 +269,12 @@ __device__ STG_AI inline void fill_zeros(const ZeroArgs &z)
 
 // ---------------------------------------------------------------- gradient: few tokens
 
-// Workgroups 0 .. tokens-1: the row of token blockIdx.x, if it is the first of
-// its id.  The others: zeros to EMBED_ZR rows of dE each that have no token.
-// blockIdx.y cuts the columns, 512 (a wave's 64 x 8) each.  Bound by its chain
-// of latencies: the token's own row, and dE's, are loaded beside the search.
-constexpr int EMBED_ZR = 32;
+// dE's zeros, alone.
+__global__ __launch_bounds__(512) void k_embed_zero(ZeroArgs z) { fill_zeros<512>(z); }
 
+// The row of token blockIdx.x, if it is the first of its id.  blockIdx.y cuts
+// the columns, 512 (a wave's 64 x 8) each.  Bound by its chain of latencies: the
+// token's own row, and dE's, are loaded beside the search.
 template <int YK, int DK>
 __global__ __launch_bounds__(256) void k_embed_grad_small(EmbedArgs a)
 {
@@ -280,32 +289,12 @@ __global__ __launch_bounds__(256) void k_embed_grad_small(EmbedArgs a)
     for (int i = 0; i < PER; ++i)
         id[i] = i * 256 + tid < T ? embed_id(a, i * 256 + tid) : -1;
     const Cols k = lane_cols(a, ((int64_t)blockIdx.y * 64 + lane) * 8);
-    if (me >= T) {
-        const int64_t r0 = (int64_t)(me - T) * EMBED_ZR;
-        if (tid < EMBED_ZR)
-            list[tid] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int64_t r = id[i] - r0;
-            if (id[i] >= 0 && r >= 0 && r < EMBED_ZR)
-                list[r] = 1;
-        }
-        __syncthreads();
-        const float z[8] = {};
-        with_full(a, k, [&](auto full) STG_AI {
-            for (int r = wave; r < EMBED_ZR; r += 4)
-                if (r0 + r < a.vocab && !list[r] && k.n > 0)
-                    store_raw<DK, decltype(full)::value>(a.out, (r0 + r) * a.ld_out + k.c, k.n, z);
-        });
-        return;
-    }
     const int mine = embed_id(a, me);
     if (mine < 0)
         return;
-    with_full(a, k, [&](auto full) STG_AI {
+    with_full(a, [&](auto full) STG_AI {
         constexpr bool FULL = decltype(full)::value;
-        const Raw8<YK> own = load_raw<YK, FULL>(a.in, me * a.ld_in + k.c, k.n);
+        const Raw8<YK> own = load_cols<YK, FULL>(a.in, me * a.ld_in, k);
         const Raw8<DK> old = get_row<DK, FULL>(a, mine, k);
         // tokens of this id by their numbers; an earlier one has the row
         bool early = false;
@@ -347,7 +336,7 @@ __global__ __launch_bounds__(256) void k_embed_grad_small(EmbedArgs a)
             Raw8<YK> r[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) // (past the end: the last one again)
-                r[q] = load_raw<YK, FULL>(a.in, list[min(k0 + q, end - 1)] * a.ld_in + k.c, k.n);
+                r[q] = load_cols<YK, FULL>(a.in, list[min(k0 + q, end - 1)] * a.ld_in, k);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
                 if (k0 + q < end) {
@@ -630,7 +619,7 @@ __global__ __launch_bounds__(256) void k_embed_runs(EmbedArgs a)
     key = p0 + lane >= 1 && p0 + lane <= n && lane < cnt + 2 ? key : -1;
     tok = lane >= 1 && lane <= cnt ? tok : 0;
     const Cols k = lane_cols(a, ((int64_t)blockIdx.y * 64 + lane) * 8);
-    with_full(a, k, [&](auto full) STG_AI {
+    with_full(a, [&](auto full) STG_AI {
         constexpr bool FULL = decltype(full)::value;
         // (32 rows of 16 bits at once: a load behind a store waits for it)
         constexpr int B = YK == OUT_F32 ? 8 : 16;
@@ -638,7 +627,7 @@ __global__ __launch_bounds__(256) void k_embed_runs(EmbedArgs a)
 #pragma unroll
             for (int q = 0; q < B; ++q) { // (past the end: the last one again)
                 const int t = __builtin_amdgcn_readlane(tok, min(i0 + q, cnt));
-                r[q] = load_raw<YK, FULL>(a.in, t * a.ld_in + k.c, k.n);
+                r[q] = load_cols<YK, FULL>(a.in, t * a.ld_in, k);
             }
         };
         float acc[8] = {};
@@ -658,9 +647,8 @@ __global__ __launch_bounds__(256) void k_embed_runs(EmbedArgs a)
                     if (i == cnt || next != id) {
                         const bool before = first == 1 && __builtin_amdgcn_readlane(key, 0) == id;
                         if (before || next == id) {
-                            if (k.n > 0)
-                                store_raw<OUT_F32, FULL>(
-                                    a.part, (run * 2 + (first > 1)) * a.cols + k.c, k.n, acc);
+                            store_cols<OUT_F32, FULL>(a.part, (run * 2 + (first > 1)) * a.cols, k,
+                                                      acc);
                         } else {
                             put_row<DK, FULL>(a, id, k, acc, get_row<DK, FULL>(a, id, k));
                         }
@@ -729,7 +717,7 @@ __global__ __launch_bounds__(512) void k_embed_join(EmbedArgs a)
             break;
     }
     const Cols k = lane_cols(a, ((int64_t)blockIdx.y * 64 + lane) * 8);
-    with_full(a, k, [&](auto full) STG_AI {
+    with_full(a, [&](auto full) STG_AI {
         constexpr bool FULL = decltype(full)::value;
         const Raw8<DK> old = get_row<DK, FULL>(a, id, k);
         // part 0 is this run's, part i run + i's
@@ -742,8 +730,8 @@ __global__ __launch_bounds__(512) void k_embed_join(EmbedArgs a)
 #pragma unroll
             for (int q = 0; q < B; ++q) {
                 const int i = min(i0 + q, i1 - 1);
-                r[q] = load_raw<OUT_F32, FULL>(
-                    a.part, ((run + i) * 2 + (i == 0 ? slot : 0)) * a.cols + k.c, k.n);
+                r[q] = load_cols<OUT_F32, FULL>(a.part,
+                                                ((run + i) * 2 + (i == 0 ? slot : 0)) * a.cols, k);
             }
 #pragma unroll
             for (int q = 0; q < B; ++q)
@@ -824,16 +812,39 @@ hipError_t launch_embed(const EmbedArgs &a, hipStream_t s)
 hipError_t launch_embed_backward(const EmbedArgs &a, hipStream_t s)
 {
     const unsigned parts = (unsigned)((a.cols + 511) / 512);
+    // rows [r0, r1) of dE's zeros by workgroups of nt threads behind `sorters`
+    auto zeros = [&](int64_t r0, int64_t r1, int sorters, int nt, ZeroArgs &z) {
+        const int64_t eb = elem_bytes(a.e_kind), rows = r1 - r0;
+        z.first = (sorters + 7) / 8 * 8;
+        z.lo = z.at = (uint8_t *)a.out + r0 * a.ld_out * eb;
+        int64_t wgs;
+        if (a.ld_out == a.cols) {
+            z.hi = z.lo + rows * a.cols * eb;
+            z.at = (uint8_t *)((uintptr_t)z.lo & ~(uintptr_t)127);
+            z.per = ((z.hi - z.at + 7) / 8 + 127) / 128 * 128;
+            wgs = (z.per + nt * 16 - 1) / (nt * 16);
+        } else {
+            z.rows = rows;
+            z.row = a.cols * eb;
+            z.pitch = a.ld_out * eb;
+            z.per = (rows + 7) / 8;
+            wgs = (z.per + nt / 64 - 1) / (nt / 64);
+        }
+        return z.first - sorters + 8 * (unsigned)(wgs < (1 << 16) ? wgs : 1 << 16);
+    };
     if (a.tokens <= EMBED_SMALL) {
-        const int64_t zero = a.accumulate ? 0 : (a.vocab + EMBED_ZR - 1) / EMBED_ZR;
-        if (a.tokens + zero == 0)
-            return hipSuccess;
-        with_kind(a.y_kind, [&](auto yk) {
-            with_kind(a.e_kind, [&](auto dk) {
-                hipLaunchKernelGGL((k_embed_grad_small<decltype(yk)::value, decltype(dk)::value>),
-                                   dim3((unsigned)(a.tokens + zero), parts), dim3(256), 0, s, a);
+        if (!a.accumulate) {
+            ZeroArgs z{};
+            const unsigned n = zeros(0, a.vocab, 0, 512, z);
+            hipLaunchKernelGGL(k_embed_zero, dim3(n), dim3(512), 0, s, z);
+        }
+        if (a.tokens > 0)
+            with_kind(a.y_kind, [&](auto yk) {
+                with_kind(a.e_kind, [&](auto dk) {
+                    hipLaunchKernelGGL((k_embed_grad_small<decltype(yk)::value, decltype(dk)::value>),
+                                       dim3((unsigned)a.tokens, parts), dim3(256), 0, s, a);
+                });
             });
-        });
         return hipGetLastError();
     }
     // a third of dE's zeros beside each of the sort's launches
@@ -841,26 +852,8 @@ hipError_t launch_embed_backward(const EmbedArgs &a, hipStream_t s)
         ZeroArgs z{};
         unsigned n = 0;
         z.first = INT_MAX;
-        if (!a.accumulate) {
-            const int64_t r0 = a.vocab * third / 3, rows = a.vocab * (third + 1) / 3 - r0;
-            const int64_t eb = elem_bytes(a.e_kind);
-            z.first = (sorters + 7) / 8 * 8;
-            z.lo = z.at = (uint8_t *)a.out + r0 * a.ld_out * eb;
-            int64_t wgs;
-            if (a.ld_out == a.cols) {
-                z.hi = z.lo + rows * a.cols * eb;
-                z.at = (uint8_t *)((uintptr_t)z.lo & ~(uintptr_t)127);
-                z.per = ((z.hi - z.at + 7) / 8 + 127) / 128 * 128;
-                wgs = (z.per + nt * 16 - 1) / (nt * 16);
-            } else {
-                z.rows = rows;
-                z.row = a.cols * eb;
-                z.pitch = a.ld_out * eb;
-                z.per = (rows + 7) / 8;
-                wgs = (z.per + nt / 64 - 1) / (nt / 64);
-            }
-            n = z.first - sorters + 8 * (unsigned)(wgs < (1 << 16) ? wgs : 1 << 16);
-        }
+        if (!a.accumulate)
+            n = zeros(a.vocab * third / 3, a.vocab * (third + 1) / 3, sorters, nt, z);
         hipLaunchKernelGGL(kernel, dim3(sorters + n), dim3(nt), lds, s, a, z);
     };
     const int lows = 1 << a.lo_bits, highs = 1 << a.hi_bits;
