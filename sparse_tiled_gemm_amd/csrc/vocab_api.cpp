@@ -19,6 +19,7 @@ struct gemm_xent_plan {
     int64_t hp;         // hidden in whole 16-byte chunks
     int copy;           // W goes through the workspace
     int stats, g, dx, dw; // XentTile of each product
+    int dw_tile;        // of dW where it is not aligned to 16 bytes
     int64_t piece;      // columns of a piece
     XentSplits split;   // of dX's sums, by the rows that have a target
     int64_t acc;        // fp32 values that they take
@@ -311,13 +312,16 @@ static void choose(gemm_xent_plan_t &p, int num_cu)
     const int64_t cols = d.vocab < p.piece ? d.vocab : p.piece;
     p.stats = choose_logits(d.tokens, p.copy ? cols : d.vocab, p.hp, num_cu);
     p.g = choose_logits(d.tokens, cols, p.hp, num_cu);
-    p.dw = best_tile(cols, p.hp, d.tokens, num_cu);
+    p.dw = p.dw_tile = best_tile(cols, p.hp, d.tokens, num_cu);
+    const int64_t dw_row = d.lddw * float_bytes(d.dw_type);
+    if (d.tokens > 0 && d.tokens <= XENT_DW_ROWS && d.hidden % 8 == 0 && dw_row % 16 == 0)
+        p.dw = XT_STREAM;
     p.dx = choose_dx(d.tokens, p.hp, cols, num_cu);
     if (const char *force = getenv("STGEMM_FORCE_KERNEL")) {
         static const char *const names[XT_COUNT] = {"tiled64", "tiled128", "tiled256"};
         for (int t = 0; t < XT_COUNT; ++t)
             if (strcmp(force, names[t]) == 0)
-                p.stats = p.g = p.dw = p.dx = t;
+                p.stats = p.g = p.dw = p.dw_tile = p.dx = t;
     }
     // dX's sums run over the piece's columns, cut where its tiles would leave
     // compute units idle.  The kernels choose by the rows that have a target;
@@ -391,9 +395,12 @@ gemm_status_t gemm_xent_plan(const gemm_xent_desc_t *desc, gemm_xent_plan_t **ou
     p->device = dev;
     choose(*p, di.num_cu);
     auto logits = [](int t) { return t == XT_STREAM ? XENT_STREAM_ROWS : xent_edge(t); };
-    snprintf(p->name, sizeof p->name, "xent_%s_stats%d_g%d_dx%d_dw%d%s",
+    char dw[16] = "rows";
+    if (p->dw != XT_STREAM)
+        snprintf(dw, sizeof dw, "%d", xent_edge(p->dw));
+    snprintf(p->name, sizeof p->name, "xent_%s_stats%d_g%d_dx%d_dw%s%s",
              p->d.x_type == GEMM_BF16 ? "bf16" : "f16", logits(p->stats), logits(p->g),
-             xent_edge(p->dx), xent_edge(p->dw), p->copy ? "_copy" : "");
+             xent_edge(p->dx), dw, p->copy ? "_copy" : "");
     static const bool log = [] {
         const char *v = getenv("GEMM_LOG");
         return v && *v && strcmp(v, "0") != 0;
@@ -568,7 +575,9 @@ gemm_status_t gemm_xent_backward(const gemm_xent_plan_t *plan, const void *X, co
             const int vec = aligned(w, 4 * (size_t)wb) && d.lddw % 4 == 0 &&
                             d.lddw * wb < 0x7fffffff / 257;
             const int lines = aligned(w, 128) && (d.lddw * wb) % 128 == 0;
-            LAUNCH(launch_xent_dw(plan->dw, a, p,
+            // (the streaming kernel stores 16 bytes at a time)
+            const int tile = vec && aligned(w, 16) ? plan->dw : plan->dw_tile;
+            LAUNCH(launch_xent_dw(tile, a, p,
                                   {w, d.lddw, out_kind(d.dw_type), d.accumulate, vec, lines}, s));
         }
     }

@@ -54,7 +54,8 @@ enum XentTile {
     XT_128,
     XT_256,
     XT_COUNT,
-    XT_STREAM = XT_COUNT // the logits of up to 16 rows: no tiles, columns in turn
+    XT_STREAM = XT_COUNT // few rows, no tiles: the logits of up to 16 (columns in
+                         // turn), dW of up to 128 (rows in turn)
 };
 inline int xent_edge(int t) { return t == XT_256 ? 256 : t == XT_128 ? 128 : 64; }
 
@@ -90,6 +91,7 @@ struct XentSplits {
 // Workgroups of the streaming kernel, four waves with 16 columns at a time
 // each: two to a compute unit.
 constexpr int XENT_STREAM_ROWS = 16;
+constexpr int XENT_DW_ROWS = 128; // rows of dW's streaming kernel
 inline int64_t xent_streams(int64_t n, int num_cu)
 {
     const int64_t g = (n + 63) / 64;

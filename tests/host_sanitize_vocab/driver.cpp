@@ -140,7 +140,12 @@ hipError_t launch_xent_dx(int tile, const XentArgs &a, const XentPiece &p, const
 hipError_t launch_xent_dw(int tile, const XentArgs &a, const XentPiece &p, const XentDw &d, hipStream_t)
 {
     check_g(a, p);
-    EXPECT(d.dW && d.ldd >= a.hidden && tile < XT_COUNT);
+    EXPECT(d.dW && d.ldd >= a.hidden && tile <= XT_STREAM);
+    if (tile == XT_STREAM) {
+        EXPECT(a.tokens > 0 && a.tokens <= XENT_DW_ROWS && a.hidden % 8 == 0 && d.vec);
+        EXPECT((uintptr_t)d.dW % 16 == 0 && d.ldd * (d.d_kind == OUT_F32 ? 4 : 2) % 16 == 0);
+        return hipSuccess;
+    }
     const int64_t b = xent_edge(tile);
     EXPECT((p.n + b - 1) / b * ((a.hp + b - 1) / b) * 512 < ((int64_t)1 << 32));
     EXPECT(!d.vec || ((uintptr_t)d.dW % 8 == 0 && d.ldd % 4 == 0));

@@ -124,6 +124,15 @@ def test_odd_widths_and_strides(dtype, tokens, vocab, hidden, pad, off, piece):
     run(tokens, vocab, hidden, dtype, dx=dtype, dw="f32", pad=pad, off=off, piece=piece, id_bytes=4)
 
 
+@pytest.mark.parametrize("tokens,vocab,hidden,pad,dtype,dw,accumulate", [
+    (40, 33001, 1024, 0, "bf16", "bf16", False), (64, 20011, 1032, 8, "f16", "f16", True),
+    (100, 33001, 1024, 0, "f16", "f32", False), (128, 20011, 1032, 8, "bf16", "f32", True),
+    (3, 33001, 1048, 0, "bf16", "f16", True), (65, 20011, 1024, 0, "f16", "bf16", True)])
+def test_few_rows_many_columns(tokens, vocab, hidden, pad, dtype, dw, accumulate):
+    """Up to 128 rows dW's rows are written in turn, several steps a wave."""
+    run(tokens, vocab, hidden, dtype, dx="f32", dw=dw, pad=pad, accumulate=accumulate)
+
+
 @pytest.mark.parametrize("dx", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("dw", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("accumulate", [False, True])
