@@ -278,28 +278,43 @@ __global__ __launch_bounds__(256, 2) void k_xent_small(XentArgs a, XentPiece p, 
 // the stream stops neither for a barrier nor for an epilogue; X's fragments come
 // from L2 beside them.  The statistics are kept per lane while the groups pass,
 // the running maximum and the sum relative to it, and joined once at the end:
-// one pair per row and workgroup.  Every step has eight vector-memory
-// instructions (past the last one they load zeros without touching memory), so
-// a step's have arrived when 3 x 8 newer ones are left.  One row, 32768 x 2048
-// (128 MB not in the caches; a plain read of it takes 21 us): the pass 33.5 us,
-// with 64-value tiles and eight buffers 34.2, with five buffers 35.7, with 64 x
-// 64 tiles 37.0.
+// one pair per row and workgroup.  Every step has eight (LOOSE: nine)
+// vector-memory instructions (past the last one they load zeros without touching
+// memory), so a step's have arrived when those of three newer steps are left.
+// A wave begins each row at a K tile of its own and goes round (rows of 4096 bytes
+// lie alike in the memory's channels, and all waves read the same ones at a time
+// otherwise), and an XCD's waves take neighbouring groups.  One row, 32768 x 2048
+// (128 MB not in the caches; a plain read of it takes 21 us): the pass 25.3 us,
+// without the latter 27.1, without either 33.4; then also with 64-value tiles and
+// eight buffers 34.2, with five buffers 35.7, with 64 x 64 tiles 37.0; with four
+// times the workgroups, 131072 columns of 4096 207 us for 202.
+// LOOSE: W's rows begin at any element.  The copies then begin at the 16 bytes
+// that hold a row's first value (all groups of 16 rows lie alike in them) and
+// take one piece more, and the fragments are read by dwords from where they
+// begin; what lies behind a row is masked.  Four rows, 196647 x 1909,
+// fp16: 141 us (5.3 TB/s; a copy of W and the pass over it took 475, unaligned
+// loads into registers 455).
 constexpr int ST_BUF = 4;
-template <class OP, bool GRAD>
-__global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p, int groups)
+template <class OP, bool GRAD, bool LOOSE>
+__global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p, int all_groups)
 {
     constexpr bool BF = std::is_same<OP, Op16BF16>::value;
-    __shared__ __attribute__((aligned(1024))) uint8_t b0[16384], b1[16384], b2[16384], b3[16384];
+    constexpr int DMAS = LOOSE ? 5 : 4, SB = DMAS * 1024; // copies of a step, their bytes
+    __shared__ __attribute__((aligned(1024))) uint8_t b0[4 * SB], b1[4 * SB], b2[4 * SB], b3[4 * SB];
     const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = gridDim.x * 4;
+    // every XCD takes an eighth of the groups, its waves every `waves`th of them
+    const int xcds = gridDim.x % 8 ? 1 : 8, share = (all_groups + xcds - 1) / xcds;
+    const int waves = gridDim.x / xcds * 4;
+    const int g0 = blockIdx.x % xcds * share + blockIdx.x / xcds * 4 + wave;
+    const int groups = min(all_groups, (int)(blockIdx.x % xcds + 1) * share);
     const int n = xent_rows(a), KT = (int)((a.hp + 127) / 128);
     const int64_t kb = a.hp * 2, ldw = p.ldw * 2, lda = (a.direct ? a.ldx : a.ldc) * 2;
     const __amdgpu_buffer_rsrc_t ra =
         tile_rsrc(a.direct ? a.X : a.Xc, n > 0 ? (n - 1) * lda + kb : 0);
     auto buf = [&](auto slot) STG_AI {
         constexpr int S = decltype(slot)::value;
-        return (S == 0 ? b0 : S == 1 ? b1 : S == 2 ? b2 : b3) + wave * 4096;
+        return (S == 0 ? b0 : S == 1 ? b1 : S == 2 ? b2 : b3) + wave * SB;
     };
     if (n == 0)
         return;
@@ -307,29 +322,42 @@ __global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p,
     const RowVals row = load_row<GRAD, 16>(a, p, n, 0, 0, min(l16, n - 1));
     // the step whose copies are issued next, and the one that is multiplied
     const int va = l16 * (int)lda + q * 16;
-    int ig = blockIdx.x * 4 + wave, it = 0;
+    const int turn = g0 % KT;
+    int ig = g0, it = turn;
     u4_t fa[ST_BUF][4];
+    const int skew = LOOSE ? (int)((uintptr_t)p.W & 15) : 0; // of the first row
+    const int hb = (int)a.hidden * 2, lw = (int)ldw;
+    // this lane's piece of copy d: byte in the group's rows, and what is left of
+    // its row from there
+    int piece[DMAS], left[DMAS];
+#pragma unroll
+    for (int d = 0; d < DMAS; ++d) {
+        const int row = d < 4 ? 4 * d + q : l16, chunk = d < 4 ? (l16 ^ row) * 16 : 256;
+        const int at = row * lw + skew;
+        piece[d] = (LOOSE ? at & ~15 : at) + chunk;
+        left[d] = d < 4 || lane < 16 ? (LOOSE ? hb + (at & 15) : (int)kb) - chunk : 0;
+    }
+    // LOOSE: this lane's fragment begins `sub` bytes into dword `dw` of its 16 bytes
+    const int dw = ((l16 * lw + skew) & 15) >> 2, sub = (l16 * lw + skew) & 2;
     auto issue = [&](auto slot) STG_AI {
         constexpr int S = decltype(slot)::value;
         const bool in = ig < groups;
         const int64_t c = (int64_t)ig * 16;
-        const __amdgpu_buffer_rsrc_t rb = epi_rsrc((const uint8_t *)p.W + (in ? c * ldw : 0),
-                                                   in ? (p.n - c - 1) * ldw + kb : 0);
+        const __amdgpu_buffer_rsrc_t rb =
+            epi_rsrc((const uint8_t *)p.W - skew + (in ? c * ldw : 0),
+                     in ? LOOSE ? ((p.n - c - 1) * ldw + hb + skew + 15) & ~(int64_t)15
+                                : (p.n - c - 1) * ldw + kb
+                        : 0);
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const int row = 4 * d + q, chunk = (l16 ^ row) * 16;
-            const bool kin = it * 256 + chunk < kb;
-            dma16(rb, buf(slot) + 1024 * d, kin ? row * (int)ldw + chunk : (int)0x80000000, it * 256);
-        }
+        for (int d = 0; d < DMAS; ++d)
+            dma16(rb, buf(slot) + 1024 * d, it * 256 < left[d] ? piece[d] : (int)0x80000000, it * 256);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const bool ain = in && it * 256 + 64 * k + q * 16 < kb;
             fa[S][k] = buf_load16(ra, ain ? va + 64 * k : (int)0x80000000, it * 256);
         }
-        if (++it == KT) {
-            it = 0;
-            ig += waves;
-        }
+        it = it + 1 < KT ? it + 1 : 0;
+        ig += it == turn ? waves : 0;
     };
     auto all = [&](auto &&f) STG_AI {
         [&]<int... I>(std::integer_sequence<int, I...>) STG_AI {
@@ -358,7 +386,7 @@ __global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p,
             cl[r] = __shfl(row.cl, 4 * q + r);
         }
     }
-    int g = blockIdx.x * 4 + wave, t = 0;
+    int g = g0, t = turn;
     // (four sums of a quarter of the values each: their roundings are smaller
     // than one sum's, and no product waits for the one before)
     typename OP::acc_t part[4] = {};
@@ -396,24 +424,46 @@ __global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p,
     auto step = [&](auto slot) STG_AI {
         constexpr int S = decltype(slot)::value;
         in_order();
-        STG_WAIT_VMCNT((ST_BUF - 1) * 8);
+        STG_WAIT_VMCNT((ST_BUF - 1) * (DMAS + 4));
         in_order();
         u4_t fb[4], x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            fb[k] = *(const u4_t *)(buf(slot) + l16 * 256 + (((4 * k + q) ^ l16) << 4));
+            const uint8_t *const b = buf(slot);
+            if constexpr (LOOSE) {
+                uint32_t w[5];
+#pragma unroll
+                for (int i = 0; i < 5; ++i) {
+                    const int chunk = 4 * k + q + ((dw + i) >> 2), in = ((dw + i) & 3) * 4;
+                    w[i] = *(const uint32_t *)(b + in + (chunk < 16 ? l16 * 256 + ((chunk ^ l16) << 4)
+                                                                    : 4096 + l16 * 16));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    fb[k][i] = __builtin_amdgcn_alignbyte(w[i + 1], w[i], sub);
+            } else {
+                fb[k] = *(const u4_t *)(b + l16 * 256 + (((4 * k + q) ^ l16) << 4));
+            }
             x[k] = fa[S][k];
         }
         wave_lds_sync(); // read before the buffer is copied into again
+        if (LOOSE && t == KT - 1)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int n = (int)a.hidden - (t * 128 + 32 * k + 8 * q); // values of the row
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    fb[k][i] &= (2 * i < n ? 0xFFFFu : 0u) | (2 * i + 1 < n ? 0xFFFF0000u : 0u);
+            }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             part[k] = OP::mma((const uint32_t *)&x[k], (const uint32_t *)&fb[k], part[k]);
         in_order();
         issue(slot);
         in_order();
-        if (++t == KT) {
+        t = t + 1 < KT ? t + 1 : 0;
+        if (t == turn) {
             finish();
-            t = 0;
             g += waves;
         }
     };
@@ -456,8 +506,15 @@ template <class OP, bool GRAD>
 static hipError_t launch_t(int tile, const XentArgs &a, const XentPiece &p, hipStream_t s)
 {
     if (tile == XT_STREAM) {
-        hipLaunchKernelGGL((k_xent_stream<OP, GRAD>), dim3((unsigned)xent_streams(p.n, a.dx.num_cu)),
-                           dim3(256), 0, s, a, p, (int)((p.n + 15) / 16));
+        const dim3 grid((unsigned)xent_streams(p.n, a.dx.num_cu));
+        const int groups = (int)((p.n + 15) / 16);
+        if constexpr (!GRAD)
+            if (p.loose) {
+                hipLaunchKernelGGL((k_xent_stream<OP, GRAD, true>), grid, dim3(256), 0, s, a, p,
+                                   groups);
+                return hipGetLastError();
+            }
+        hipLaunchKernelGGL((k_xent_stream<OP, GRAD, false>), grid, dim3(256), 0, s, a, p, groups);
         return hipGetLastError();
     }
     const int64_t b = xent_edge(tile);

@@ -18,6 +18,7 @@ struct gemm_xent_plan {
     gemm_xent_desc_t d; // normalised: packed leading dimensions filled in
     int64_t hp;         // hidden in whole 16-byte chunks
     int copy;           // W goes through the workspace
+    int loose;          // but not forward: the streaming kernel reads it where it lies
     int stats, g, dx, dw; // XentTile of each product
     int dw_tile;        // of dW where it is not aligned to 16 bytes
     int64_t piece;      // columns of a piece
@@ -253,11 +254,15 @@ static int best_tile(int64_t m, int64_t n, int64_t k, int num_cu)
     return best;
 }
 
-// Tile of the logits' product of `n` columns.
+// Tile of the logits' product of `n` columns.  Up to 16 rows the streaming
+// kernel, but 64 x 64 tiles for long rows of a W of 512 MB and more: 1 row,
+// 131072 x 4096, 183 us and 166; 16 rows 204 and 168; 16, 65536 x 4096, 104 and
+// 100; 4, 32768 x 8192, 100 and 104; 10, 50021 x 1416, 38 and 37; 9, 200000 x
+// 512, 39 and 49; 1, 32768 x 2048, 25 and 32.
 static int choose_logits(int64_t tokens, int64_t n, int64_t hp, int num_cu)
 {
     if (tokens <= XENT_STREAM_ROWS)
-        return XT_STREAM;
+        return hp >= 2048 && n * hp >= (1 << 28) ? XT_64 : XT_STREAM;
     return tokens <= 64 ? XT_64 : best_tile(tokens, n, hp, num_cu);
 }
 
@@ -311,6 +316,8 @@ static void choose(gemm_xent_plan_t &p, int num_cu)
     p.piece = ceil_div(ceil_div(d.vocab, n), 256) * 256;
     const int64_t cols = d.vocab < p.piece ? d.vocab : p.piece;
     p.stats = choose_logits(d.tokens, p.copy ? cols : d.vocab, p.hp, num_cu);
+    if (p.copy && d.tokens <= XENT_STREAM_ROWS) // (no copy of W: see loose)
+        p.stats = XT_STREAM;
     p.g = choose_logits(d.tokens, cols, p.hp, num_cu);
     p.dw = p.dw_tile = best_tile(cols, p.hp, d.tokens, num_cu);
     const int64_t dw_row = d.lddw * float_bytes(d.dw_type);
@@ -323,6 +330,7 @@ static void choose(gemm_xent_plan_t &p, int num_cu)
             if (strcmp(force, names[t]) == 0)
                 p.stats = p.g = p.dw = p.dw_tile = p.dx = t;
     }
+    p.loose = p.copy && p.stats == XT_STREAM && d.tokens <= XENT_STREAM_ROWS && d.ldw < (1 << 21);
     // dX's sums run over the piece's columns, cut where its tiles would leave
     // compute units idle.  The kernels choose by the rows that have a target;
     // here every number of them needs room.
@@ -338,6 +346,8 @@ static void choose(gemm_xent_plan_t &p, int num_cu)
         p.split.wgs = wgs > p.split.wgs ? wgs : p.split.wgs;
     }
 }
+
+static bool copy_forward(const gemm_xent_plan_t &p) { return p.copy && !p.loose; }
 
 // Maxima and sums per row that the statistics of n columns leave.
 static int64_t stats_parts(const gemm_xent_plan_t &p, int64_t n)
@@ -368,12 +378,12 @@ static size_t xent_parts(const gemm_xent_plan_t &p, bool backward, void *workspa
         piece.ldg = p.piece;
     } else {
         const int64_t full = d.vocab / p.piece;
-        a.part_tiles = p.copy ? full * stats_parts(p, p.piece) + stats_parts(p, d.vocab - full * p.piece)
+        a.part_tiles = copy_forward(p) ? full * stats_parts(p, p.piece) + stats_parts(p, d.vocab - full * p.piece)
                               : stats_parts(p, d.vocab);
         w.take(a.zt, d.tokens);
         w.take(a.part, a.part_tiles * d.tokens * 2);
     }
-    if (p.copy)
+    if (backward ? p.copy : copy_forward(p))
         w.take(copy, (d.vocab < p.piece ? d.vocab : p.piece) * a.ldc);
     return w.at;
 }
@@ -474,13 +484,14 @@ static gemm_status_t check_call(const gemm_xent_plan_t &p, const void *W)
 }
 
 // W's rows of a piece: where they lie, or copied.
-static hipError_t take_w(const gemm_xent_plan_t &p, const void *W, uint16_t *copy, XentPiece &piece,
-                         hipStream_t s)
+static hipError_t take_w(const gemm_xent_plan_t &p, bool copies, const void *W, uint16_t *copy,
+                         XentPiece &piece, hipStream_t s)
 {
     const uint16_t *w = (const uint16_t *)W + piece.v0 * p.d.ldw;
-    piece.W = p.copy ? copy : w;
-    piece.ldw = p.copy ? xent_pitch(p.d.hidden) : p.d.ldw;
-    return p.copy ? launch_xent_copy({w, p.d.ldw, piece.n, p.d.hidden, p.hp, copy, piece.ldw}, s) : hipSuccess;
+    piece.W = copies ? copy : w;
+    piece.ldw = copies ? xent_pitch(p.d.hidden) : p.d.ldw;
+    return copies ? launch_xent_copy({w, p.d.ldw, piece.n, p.d.hidden, p.hp, copy, piece.ldw}, s)
+                  : hipSuccess;
 }
 
 #define LAUNCH(x)                                 \
@@ -520,10 +531,12 @@ gemm_status_t gemm_xent_forward(const gemm_xent_plan_t *plan, const void *X, con
                aligned(X, 16);
     if (!a.direct)
         LAUNCH(launch_xent_prepare(a, false, s));
-    const int64_t step = plan->copy ? plan->piece : d.vocab;
+    const bool copies = copy_forward(*plan);
+    const int64_t step = copies ? plan->piece : d.vocab;
+    p.loose = plan->loose;
     for (p.v0 = 0; p.v0 < d.vocab; p.v0 += step) {
         p.n = d.vocab - p.v0 < step ? d.vocab - p.v0 : step;
-        LAUNCH(take_w(*plan, W, copy, p, s));
+        LAUNCH(take_w(*plan, copies, W, copy, p, s));
         LAUNCH(launch_xent_stats(plan->stats, a, p, s));
         p.tile0 += stats_parts(*plan, p.n);
     }
@@ -564,7 +577,7 @@ gemm_status_t gemm_xent_backward(const gemm_xent_plan_t *plan, const void *X, co
     LAUNCH(launch_xent_prepare(a, true, s));
     for (p.v0 = 0; p.v0 < d.vocab; p.v0 += plan->piece) {
         p.n = d.vocab - p.v0 < plan->piece ? d.vocab - p.v0 : plan->piece;
-        LAUNCH(take_w(*plan, W, copy, p, s));
+        LAUNCH(take_w(*plan, plan->copy, W, copy, p, s));
         if (t > 0)
             LAUNCH(launch_xent_g(plan->g, a, p, s));
         if (dX && t > 0)

@@ -125,8 +125,9 @@ struct XentArgs {
 
 // One piece of the vocabulary: columns v0 .. v0 + n - 1.
 struct XentPiece {
-    const void *W; // its first row, 16-byte aligned
+    const void *W; // its first row, rows 16-byte aligned unless loose
     int64_t ldw;
+    int loose; // forward, few rows: W is read where it lies, aligned or not
     int64_t v0, n;
     int64_t tile0; // forward: its first tile column in XentArgs::part
     uint16_t *G;   // backward: rows x ldg

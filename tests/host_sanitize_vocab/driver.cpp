@@ -71,8 +71,11 @@ static void check_args(const XentArgs &a, bool backward)
 }
 static void check_piece(int tile, const XentArgs &a, const XentPiece &p)
 {
-    EXPECT(p.n > 0 && p.v0 >= 0 && p.v0 + p.n <= a.vocab && p.ldw % 8 == 0 && p.ldw < (1 << 21));
-    EXPECT((uintptr_t)p.W % 16 == 0 && p.ldw >= a.hp);
+    EXPECT(p.n > 0 && p.v0 >= 0 && p.v0 + p.n <= a.vocab && (p.loose || p.ldw % 8 == 0) && p.ldw < (1 << 21));
+    if (p.loose)
+        EXPECT(!p.G && a.tokens <= XENT_STREAM_ROWS && p.ldw >= a.hidden && p.ldw < (1 << 21));
+    else
+        EXPECT((uintptr_t)p.W % 16 == 0 && p.ldw >= a.hp);
     EXPECT(tile >= 0 && (tile < XT_COUNT || (tile == XT_STREAM && a.tokens <= XENT_STREAM_ROWS)));
     if (tile < XT_COUNT) {
         const int64_t b = xent_edge(tile);

@@ -124,6 +124,15 @@ def test_odd_widths_and_strides(dtype, tokens, vocab, hidden, pad, off, piece):
     run(tokens, vocab, hidden, dtype, dx=dtype, dw="f32", pad=pad, off=off, piece=piece, id_bytes=4)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens,vocab,hidden,pad,off", [
+    (1, 1, 7, 0, 1), (1, 17, 8, 0, 1), (16, 5003, 9, 0, 0), (2, 40001, 15, 0, 3), (5, 700, 127, 1, 0),
+    (7, 700, 128, 0, 1), (16, 3000, 129, 5, 7), (13, 20011, 1031, 0, 0), (3, 5003, 1096, 4, 0)])
+def test_few_rows_of_any_alignment(dtype, tokens, vocab, hidden, pad, off):
+    """W read where it lies, NaN between its rows."""
+    run(tokens, vocab, hidden, dtype, pad=pad, off=off)
+
+
 @pytest.mark.parametrize("tokens,vocab,hidden,pad,dtype,dw,accumulate", [
     (40, 33001, 1024, 0, "bf16", "bf16", False), (64, 20011, 1032, 8, "f16", "f16", True),
     (100, 33001, 1024, 0, "f16", "f32", False), (128, 20011, 1032, 8, "bf16", "f32", True),
