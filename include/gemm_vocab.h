@@ -95,7 +95,8 @@ gemm_status_t gemm_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, i
  * and at most 2^36 logits.
  * Where hidden or ldw is no multiple of 8, or W is not 16-byte aligned
  * (`unaligned` = 1 makes room for that; GEMM_ERR_MISALIGNED without it), W is
- * copied to the workspace piece by piece. */
+ * copied to the workspace piece by piece; the forward pass of up to 16 tokens
+ * reads it where it lies. */
 typedef struct {
     int64_t tokens, vocab, hidden;
     int32_t x_type, dx_type, dw_type; /* gemm_dtype_t */

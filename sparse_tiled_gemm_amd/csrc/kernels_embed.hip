@@ -3,7 +3,7 @@
 // The lookup Y[t] = s E[id_t] is one pass of 16-byte pieces; bound by memory.
 //
 // The gradient dE[v] = s sum of dY[t] over the tokens t of row v needs the
-// tokens grouped by row.  Up to EMBED_SMALL tokens one launch (behind one
+// tokens grouped by row.  For few tokens (embed_small) one launch (behind one
 // that writes the zeros, if the whole gradient is written) does it without a sort: a workgroup per token looks through all ids, leaves if an earlier
 // token has its id, and sums the rows of the later ones otherwise.  More
 // tokens are sorted in two stable passes, by the low bits of the id (counts
@@ -272,23 +272,26 @@ __device__ STG_AI inline void fill_zeros(const ZeroArgs &z)
 // dE's zeros, alone.
 __global__ __launch_bounds__(512) void k_embed_zero(ZeroArgs z) { fill_zeros<512>(z); }
 
-// The row of token blockIdx.x, if it is the first of its id.  blockIdx.y cuts
-// the columns, 512 (a wave's 64 x 8) each.  Bound by its chain of latencies: the
-// token's own row, and dE's, are loaded beside the search.
-template <int YK, int DK>
-__global__ __launch_bounds__(256) void k_embed_grad_small(EmbedArgs a)
+// The row of token blockIdx.x, if it is the first of its id: P parts of 512
+// columns (a wave's 64 x 8), four waves each.  Bound by its chain of latencies (the
+// token's own row, and dE's, are loaded beside the search), and by the search
+// where there are many: a workgroup per part took 8.9 us for 512 tokens of 2048
+// columns, one for the four 6.8, and 56 and 26 for 2048 of 1104.  MAX: tokens.
+template <int YK, int DK, int P, int MAX>
+__global__ __launch_bounds__(256 * P) void k_embed_grad_small(EmbedArgs a)
 {
-    constexpr int PER = EMBED_SMALL / 256;
-    __shared__ int found[PER * 4];
-    __shared__ int list[EMBED_SMALL];
-    __shared__ float red[4][64][9]; // (9: the lanes' eight values on all banks)
+    constexpr int NT = 256 * P, NW = 4 * P, PER = MAX / NT;
+    __shared__ int found[PER * NW];
+    __shared__ int list[MAX];
+    __shared__ float red[NW][64][9]; // (9: the lanes' eight values on all banks)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int part = wave % P, quarter = wave / P;
     const int T = (int)a.tokens, me = blockIdx.x;
     int id[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        id[i] = i * 256 + tid < T ? embed_id(a, i * 256 + tid) : -1;
-    const Cols k = lane_cols(a, ((int64_t)blockIdx.y * 64 + lane) * 8);
+        id[i] = i * NT + tid < T ? embed_id(a, i * NT + tid) : -1;
+    const Cols k = lane_cols(a, (((int64_t)blockIdx.y * P + part) * 64 + lane) * 8);
     const int mine = embed_id(a, me);
     if (mine < 0)
         return;
@@ -302,37 +305,37 @@ __global__ __launch_bounds__(256) void k_embed_grad_small(EmbedArgs a)
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const bool same = id[i] == mine;
-            early |= same && i * 256 + tid < me;
+            early |= same && i * NT + tid < me;
             m[i] = __ballot(same);
             if (lane == 0)
-                found[i * 4 + wave] = __popcll(m[i]);
+                found[i * NW + wave] = __popcll(m[i]);
         }
         if (__syncthreads_or(early))
             return;
         int n = 0;
-        for (int j = 0; j < PER * 4; ++j) {
+        for (int j = 0; j < PER * NW; ++j) {
             const int x = found[j];
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (j == i * 4 + wave && (m[i] >> lane & 1))
-                    list[n + lanes_below(m[i])] = i * 256 + tid;
+                if (j == i * NW + wave && (m[i] >> lane & 1))
+                    list[n + lanes_below(m[i])] = i * NT + tid;
             n += x;
         }
         float acc[8];
         if (n == 1) {
-            if (wave == 0) {
+            if (quarter == 0) {
                 widen_raw<YK>(own, acc);
                 put_row<DK, FULL>(a, mine, k, acc, old);
             }
             return;
         }
         __syncthreads();
-        // a quarter of the rows per wave, eight in flight; joined in order
-        const int per = n >= 16 ? (n + 3) / 4 : n, end = min(n, (wave + 1) * per);
+        // a quarter of the rows per wave of a part, eight in flight; joined in order
+        const int per = n >= 16 ? (n + 3) / 4 : n, end = min(n, (quarter + 1) * per);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             acc[e] = 0.0f;
-        for (int k0 = wave * per; k0 < end; k0 += 8) {
+        for (int k0 = quarter * per; k0 < end; k0 += 8) {
             Raw8<YK> r[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) // (past the end: the last one again)
@@ -348,19 +351,19 @@ __global__ __launch_bounds__(256) void k_embed_grad_small(EmbedArgs a)
                 }
         }
         if (n >= 16) {
-            if (wave)
+            if (quarter)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     red[wave][lane][e] = acc[e];
             __syncthreads();
-            if (wave == 0)
+            if (quarter == 0)
 #pragma unroll
                 for (int w = 1; w < 4; ++w)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        acc[e] += red[w][lane][e];
+                        acc[e] += red[w * P + part][lane][e];
         }
-        if (wave == 0)
+        if (quarter == 0)
             put_row<DK, FULL>(a, mine, k, acc, old);
     });
 }
@@ -832,7 +835,7 @@ hipError_t launch_embed_backward(const EmbedArgs &a, hipStream_t s)
         }
         return z.first - sorters + 8 * (unsigned)(wgs < (1 << 16) ? wgs : 1 << 16);
     };
-    if (a.tokens <= EMBED_SMALL) {
+    if (embed_small(a.tokens, a.cols)) {
         if (!a.accumulate) {
             ZeroArgs z{};
             const unsigned n = zeros(0, a.vocab, 0, 512, z);
@@ -841,8 +844,21 @@ hipError_t launch_embed_backward(const EmbedArgs &a, hipStream_t s)
         if (a.tokens > 0)
             with_kind(a.y_kind, [&](auto yk) {
                 with_kind(a.e_kind, [&](auto dk) {
-                    hipLaunchKernelGGL((k_embed_grad_small<decltype(yk)::value, decltype(dk)::value>),
-                                       dim3((unsigned)a.tokens, parts), dim3(256), 0, s, a);
+                    constexpr int YK = decltype(yk)::value, DK = decltype(dk)::value;
+                    auto go = [&](auto pc) {
+                        constexpr int P = decltype(pc)::value;
+                        const dim3 grid((unsigned)a.tokens, (parts + P - 1) / P), block(256 * P);
+                        if (a.tokens <= 1024)
+                            hipLaunchKernelGGL((k_embed_grad_small<YK, DK, P, 1024>), grid, block, 0, s, a);
+                        else
+                            hipLaunchKernelGGL((k_embed_grad_small<YK, DK, P, 2048>), grid, block, 0, s, a);
+                    };
+                    if (parts == 1)
+                        go(std::integral_constant<int, 1>{});
+                    else if (parts == 2)
+                        go(std::integral_constant<int, 2>{});
+                    else
+                        go(std::integral_constant<int, 4>{});
                 });
             });
         return hipGetLastError();

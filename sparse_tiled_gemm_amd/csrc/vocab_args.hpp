@@ -13,8 +13,16 @@ namespace stg {
 // ---------------------------------------------------------------- embedding
 
 constexpr int64_t EMBED_MAX_VOCAB = (int64_t)1 << 20;
-// up to this many tokens the gradient is one launch, without a sort
+// up to this many tokens the gradient needs no workspace
 constexpr int EMBED_SMALL = 1024;
+// Tokens that the gradient groups without a sort, every one looking through all
+// ids: 512 tokens, 2048 columns 6.8 us, 2048, 1104 26 (the sort's five launches
+// 35-40); more columns are more workgroups that look: 2048, 4096 51, but 1000, 8192
+// 34.
+inline bool embed_small(int64_t tokens, int64_t cols)
+{
+    return tokens <= EMBED_SMALL || (tokens <= 2048 && cols <= 2048);
+}
 // sorted positions whose rows one wave sums
 constexpr int EMBED_RUN = 32;
 constexpr int EMBED_MAX_BINS = 1024; // of either pass of the sort

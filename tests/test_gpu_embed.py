@@ -97,6 +97,14 @@ def test_gradient_types(y, e, tokens, vocab, cols, pad):
     run_gradient("hot", tokens, vocab, cols, y, e, True, 4, pad, 2.0)
 
 
+@pytest.mark.parametrize("kind", ["some", "hot"])
+@pytest.mark.parametrize("tokens", [1024, 1025, 2048, 2049])
+@pytest.mark.parametrize("cols", [512, 520, 1030, 2048, 2056])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_by_search_or_sort(kind, tokens, cols, accumulate):
+    run_gradient(kind, tokens, 300, cols, "bf16", "bf16", accumulate, 8, 0, 0.5)
+
+
 @pytest.mark.parametrize("tokens,vocab,cols,kind", [
     (2000, 1, 8, "one"), (2000, 2, 513, "all"), (1500, 3, 1, "all"), (40000, 65537, 24, "hot"),
     (70000, 1000, 40, "some"), (1100, 1 << 20, 8, "some"), (20000, 131072, 16, "ends"),
