@@ -3,16 +3,17 @@
 // The lookup Y[t] = s E[id_t] is one pass of 16-byte pieces; bound by memory.
 //
 // The gradient dE[v] = s sum of dY[t] over the tokens t of row v needs the
-// tokens grouped by row.  For few tokens (embed_small) one launch (behind one
-// that writes the zeros, if the whole gradient is written) does it without a sort: a workgroup per token looks through all ids, leaves if an earlier
-// token has its id, and sums the rows of the later ones otherwise.  More
-// tokens are sorted in two stable passes, by the low bits of the id (counts
-// and places of chunks, as the routing's sort) and, a workgroup per bin, by
-// the high bits.  (One launch, in which a workgroup per bin picked its tokens
-// from all ids, took 64 us for 50000 tokens, the three 40.)  A wave then sums
-// the rows of EMBED_RUN sorted positions; sums of a row that reach over several
-// runs (a frequent token) are left in the workspace and joined by a last
-// launch.  Every sum's order is a function of the ids alone.
+// tokens grouped by row.  For few tokens (embed_small) one launch does it without
+// a sort, behind one that writes the zeros if the whole gradient is written: a
+// workgroup per token looks through all ids, leaves if an earlier token has its
+// id, and sums the rows of the later ones otherwise.  More tokens are sorted in
+// two stable passes, by the low bits of the id (counts and places of chunks, as
+// the routing's sort) and, a workgroup per bin, by the high bits.  (One launch,
+// in which a workgroup per bin picked its tokens from all ids, took 64 us for
+// 50000 tokens, the three 40.)  A wave then sums the rows of EMBED_RUN sorted
+// positions; sums of a row that reach over several runs (a frequent token) are
+// left in the workspace and joined by a last launch.  Every sum's order is a
+// function of the ids alone.
 //
 // Where the whole gradient is written, zeros go to all of dE beside the
 // sort's launches, which leave most of the chip idle, and the rows that have
