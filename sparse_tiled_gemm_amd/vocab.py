@@ -12,7 +12,7 @@ operators of include/gemm_vocab.h: tokens in, loss out, and the gradients.
 E is f16 or bf16, X and dX0 have its type, dE is fp32.  ids and targets are int32 or
 int64; an id out of range is padding (a row of zeros, no gradient), a target
 out of range a token that does not count (loss and lse 0, a row of zeros in
-dX).  dloss and dlse are fp32, by token: the mean of the losses has dloss =
+dX).  dE begins as zeros, so that a new object's first call may add to it.  dloss and dlse are fp32, by token: the mean of the losses has dloss =
 1 / (number of targets).
 
 All buffers are made once and belong to the object, those it returns among
@@ -44,7 +44,8 @@ class TiedVocab:
         f32, u8 = torch.float32, torch.uint8
         self.X0, self.dX = mk(tokens, self.hidden), mk(tokens, self.hidden)
         self.loss_, self.lse = mk(tokens, d=f32), mk(tokens, d=f32)
-        self.dE = mk(self.vocab, self.hidden, d=f32)
+        # zeros, so that the first call may add to it
+        self.dE = torch.zeros((self.vocab, self.hidden), dtype=f32, device=dev)
         self.plans = {}
         # (its size is the same for every plan of this object)
         self.ws = mk(max(G.gemm_embed_workspace(tokens, self.vocab, self.hidden),

@@ -130,3 +130,31 @@ def test_gradient_of_both_ends_against_differences():
     diff = lambda h: (value(E.double() + h * d) - value(E.double() - h * d)) / (2 * h)
     d1, d2 = diff(1e-4), diff(2e-4)
     assert abs(float((dE * d).sum()) - d1) <= float((bound * d.abs()).sum()) + abs(d2 - d1)
+
+
+def test_the_first_call_may_add_to_the_gradient():
+    """embed_backward() alone, and loss_backward(accumulate=True), as a new
+    object's first call: what the overwriting calls give."""
+    tokens, vocab, hidden = 90, 300, 64
+    E = table(vocab, hidden, "bf16").cuda()
+    ids, y = (x.cuda() for x in batch(tokens, vocab, 2))
+    gen = torch.Generator().manual_seed(4)
+    X = torch.randn(tokens, hidden, generator=gen).bfloat16().cuda()
+    dloss = torch.ones(tokens, device="cuda")
+
+    def made():  # on memory that has been used
+        junk = [torch.full((vocab * hidden,), float("nan"), device="cuda") for _ in range(4)]
+        del junk
+        return TiedVocab(E, tokens)
+
+    out = []
+    for accumulate in (False, True):
+        ends = made()
+        ends.embed(ids)
+        looked_up = ends.embed_backward(X, accumulate=accumulate).clone()
+        ends = made()
+        ends.loss(X, y)
+        ends.loss_backward(dloss, accumulate=accumulate)
+        out.append((looked_up, ends.dE.clone()))
+    for a, b in zip(*out):
+        assert bool(torch.isfinite(b).all()) and torch.equal(a, b)

@@ -137,3 +137,13 @@ def test_no_graph_of_the_callers_is_kept(lib):
     ends.loss_backward(dev(torch.ones(T)).requires_grad_())
     a = lib.last("gemm_xent_backward")[0]
     assert not any(isinstance(t, torch.Tensor) and t.requires_grad for t in a)
+
+
+def test_the_gradient_starts_at_zero(lib):
+    """The first call may add to dE: embed_backward() does by default."""
+    torch.use_deterministic_algorithms(True)  # torch.empty's memory is filled with NaN
+    try:
+        ends = ends_of()
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert (ends.dE == 0).all()
