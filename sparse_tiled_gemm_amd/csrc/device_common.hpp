@@ -720,12 +720,22 @@ __device__ STG_AI inline f4_t epi_affine(const EpiArgs &e, f4_t t, f4_t b)
 // to the operand tiles; measured 2-4 % faster on MI355X with a C operand).
 constexpr int EPI_CPOL = 2; // the NT bit of the buffer instructions' cache-policy operand
 
+// 16 bytes to byte offset voff + soff.  The instruction's own scalar offset
+// stays zero: behind a 16-byte store that takes it from a register the compiler
+// overwrites the stored registers at once, and what they became has been stored;
+// behind one that does not it waits.
+template <int CPOL>
+__device__ STG_AI inline void epi_store16(__amdgpu_buffer_rsrc_t rd, int voff, int soff, u4_t w)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(w, rd, voff + soff, 0, CPOL);
+}
+
 // Store four finished values at byte offset voff + soff of the D resource.
 template <int KIND, int CPOL>
 __device__ STG_AI inline void epi_store4(__amdgpu_buffer_rsrc_t rd, int voff, int soff, f4_t y)
 {
     if constexpr (KIND == OUT_F32) {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4_t, y), rd, voff, soff, CPOL);
+        epi_store16<CPOL>(rd, voff, soff, __builtin_bit_cast(u4_t, y));
     } else if constexpr (KIND == OUT_E4M3 || KIND == OUT_E5M2) {
         constexpr bool E4 = KIND == OUT_E4M3;
         const uint32_t w = f32_to_fp8_bits<E4>(y[0]) | (f32_to_fp8_bits<E4>(y[1]) << 8) |
@@ -786,7 +796,8 @@ __device__ STG_AI inline i4_t add_c(i4_t v, i4_t c, int sat)
 // the operands as vector-aligned (e.vec), C and D are addressed through
 // buffer resources that start at the block's first row and end at row M:
 // rows past M read as zero and their stores are dropped, so no lane
-// branches, the row step between passes is a scalar offset, and all C loads
+// branches, the row step between passes is a scalar offset (added to the lane's
+// where 16 bytes are stored), and all C loads
 // of a slab are issued before the slab is staged (their latency is paid
 // once per slab).  Other blocks take an element-by-element path.
 // KIND: the output kind (OUT_S32: int32 output of an integer accumulator;
@@ -901,8 +912,7 @@ __device__ STG_AI inline void epilogue_slabs(const EpiArgs &e, typename OP::acc_
                 const int soff = (32 * i + p * RPP) * ldd_b;
                 if constexpr (IOUT) {
                     const v4_t w = has_c ? add_c(v, __builtin_bit_cast(v4_t, cv[p]), e.sat) : v;
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4_t, w), rd, vd, soff,
-                                                           CPOL);
+                    epi_store16<CPOL>(rd, vd, soff, __builtin_bit_cast(u4_t, w));
                 } else {
                     const f4_t f = has_c ? add_c(v, widen_c(cv[p], e.c_kind)) : v;
                     epi_store4<KIND, CPOL>(rd, vd, soff, epi_affine(e, f, bv));
