@@ -75,7 +75,8 @@ gemm_status_t gemm_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, i
  * tiles of the vocabulary and never kept:
  *     lse[t]  = log sum_v exp(z[t,v])
  *     loss[t] = lse[t] - z[t, targets[t]]
- * both fp32.  A token whose target is not in 0 .. vocab-1 gets loss = lse = 0;
+ * both fp32; a logit of +inf makes lse +inf, one of -inf adds nothing, a NaN makes
+ * both NaN.  A token whose target is not in 0 .. vocab-1 gets loss = lse = 0;
  * neither its row of X nor its elements of the vectors below enter anything.
  * The gradient takes lse as the forward pass wrote it, dloss[t] and dlse[t]
  * (fp32; dlse may be NULL for zeros), and makes the logits again, piece by

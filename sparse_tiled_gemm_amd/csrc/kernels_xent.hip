@@ -138,7 +138,7 @@ __global__ __launch_bounds__(256) void k_xent_loss(XentArgs a, int rows)
     const int64_t row = (int64_t)blockIdx.x * rows + (tid & (rows - 1));
     float m = -INFINITY, s = 0.0f;
     auto join = [&](float m2, float s2) STG_AI {
-        const float mx = __builtin_fmaxf(m, m2), ref = mx == -INFINITY ? 0.0f : mx;
+        const float mx = __builtin_fmaxf(m, m2), ref = sum_ref(mx);
         s = s * __builtin_amdgcn_exp2f((m - ref) * LOG2E) +
             s2 * __builtin_amdgcn_exp2f((m2 - ref) * LOG2E);
         m = mx;

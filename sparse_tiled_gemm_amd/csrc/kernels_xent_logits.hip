@@ -115,7 +115,7 @@ __device__ STG_AI inline void tile_stats(const XentArgs &a, const XentPiece &p, 
                 a.zt[m_blk + rb + 16 * i + 4 * q + r] = x;
             }
             m = max16(m);
-            const float ref = m == -INFINITY ? 0.0f : m;
+            const float ref = sum_ref(m);
 #pragma unroll
             for (int j = 0; j < S::FN; ++j)
                 s += __builtin_amdgcn_exp2f((acc[i][j][r] - ref) * LOG2E);
@@ -133,7 +133,7 @@ __device__ STG_AI inline void tile_stats(const XentArgs &a, const XentPiece &p, 
 #pragma unroll
         for (int w = 0; w < S::GN; ++w)
             m = __builtin_fmaxf(m, st[(w * S::BM + tid) * 2]);
-        const float ref = m == -INFINITY ? 0.0f : m;
+        const float ref = sum_ref(m);
 #pragma unroll
         for (int w = 0; w < S::GN; ++w)
             s += st[(w * S::BM + tid) * 2 + 1] *
@@ -414,7 +414,7 @@ __global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p,
                 if (tgt[r] == col)
                     a.zt[4 * q + r] = z;
                 const float x = col < p.n ? z : -INFINITY, mx = __builtin_fmaxf(m[r], x);
-                const float ref = mx == -INFINITY ? 0.0f : mx;
+                const float ref = sum_ref(mx);
                 s[r] = s[r] * __builtin_amdgcn_exp2f((m[r] - ref) * LOG2E) +
                        __builtin_amdgcn_exp2f((x - ref) * LOG2E);
                 m[r] = mx;
@@ -477,7 +477,7 @@ __global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p,
         float *st = (float *)b0;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const float mx = max16(m[r]), ref = mx == -INFINITY ? 0.0f : mx;
+            const float mx = max16(m[r]), ref = sum_ref(mx);
             const float sum = sum16(s[r] * __builtin_amdgcn_exp2f((m[r] - ref) * LOG2E));
             if (l16 == 0) {
                 st[(wave * 16 + 4 * q + r) * 2] = mx;
@@ -490,7 +490,7 @@ __global__ __launch_bounds__(256, 2) void k_xent_stream(XentArgs a, XentPiece p,
 #pragma unroll
             for (int w = 0; w < 4; ++w)
                 mx = __builtin_fmaxf(mx, st[(w * 16 + threadIdx.x) * 2]);
-            const float ref = mx == -INFINITY ? 0.0f : mx;
+            const float ref = sum_ref(mx);
 #pragma unroll
             for (int w = 0; w < 4; ++w)
                 sum += st[(w * 16 + threadIdx.x) * 2 + 1] *

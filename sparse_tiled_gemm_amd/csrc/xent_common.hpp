@@ -22,6 +22,14 @@ __device__ STG_AI inline int xent_row_target(const XentArgs &a, int64_t row)
     return a.direct ? xent_target(a, row) : a.tgt[row];
 }
 
+// What a sum of exponentials is relative to: their largest argument m, but zero
+// where that is infinite.  All -inf then sum to zero, and one +inf makes the sum
+// +inf as the definition does (relative to itself it would be a NaN).
+__device__ STG_AI inline float sum_ref(float m)
+{
+    return __builtin_fabsf(m) == __builtin_inff() ? 0.0f : m;
+}
+
 // The logits' gradient enters its products as a 16-bit value relative to the
 // call's largest coefficient: |G| <= 2 F with F = 1, or 2^14 for fp16, whose
 // normal values then begin at 2^-28 of that coefficient (a probability of 4e-9)
