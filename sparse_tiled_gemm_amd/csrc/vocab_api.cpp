@@ -70,7 +70,9 @@ struct Parts {
     }
 };
 
-// The sort's sizes and the workspace of the gradient.
+// The sort's sizes and the workspace of the gradient.  It depends on the number of
+// tokens alone whether there is one, also where the kernels group up to 2048
+// tokens without it (embed_small).
 size_t embed_parts(EmbedArgs &a, void *workspace)
 {
     if (a.tokens <= EMBED_SMALL)
@@ -231,8 +233,9 @@ static int64_t tiles(int t, int64_t m, int64_t n)
 // What a product of m x n outputs and a sum of k takes in a tile's rounds of
 // workgroups, us: a 64-value step of the sum and the rest of a tile's way (its
 // first operands, its epilogue), with one workgroup of 256 x 256 on a compute
-// unit and two of the others.  Fitted on the measured kernels; within some 20 %
-// of them, and in their order: 265 tokens, 19890 x 840, dW 32 / 31 / 54 us for
+// unit and two of the others.  Fitted on the measured kernels, for their order: it
+// is within some 25 % of most, and 40 to 65 % above where few tiles have a long
+// sum (the last one here).  265 tokens, 19890 x 840, dW 32 / 31 / 54 us for
 // 256 / 128 / 64 (measured 38, 31, 44); 3 tokens, 172148 x 72, 31 / 21 (41, 25);
 // 137, 32408 x 7096, 186 / 243 (220, 249); logits of 260, 58186 x 88, 24 / 23 /
 // 43 (26, 24, 35); 442, 90142 x 456, 62 / 79 (63, 77); 556, 1379 x 7920, 189 /

@@ -16,9 +16,12 @@ constexpr int64_t EMBED_MAX_VOCAB = (int64_t)1 << 20;
 // up to this many tokens the gradient needs no workspace
 constexpr int EMBED_SMALL = 1024;
 // Tokens that the gradient groups without a sort, every one looking through all
-// ids: 512 tokens, 2048 columns 6.8 us, 2048, 1104 26 (the sort's five launches
-// 35-40); more columns are more workgroups that look: 2048, 4096 51, but 1000, 8192
-// 34.
+// ids: 512 tokens, 2048 columns 6.8 us.  Added to an fp32 table, us without and
+// with the sort: 1100 tokens 17-19 / 36-39, 1500 21 / 37, 2048 25-29 / 36-39 (64 to
+// 2048 columns); more columns are more workgroups that look: 2048, 4096 51, but
+// 1000, 8192 34.  The sizes decide, and the ids may turn it: with half of the
+// tokens one id, whose rows four waves sum, 1500 30-42 / 36, 2048 37-56 / 37; with all
+// of them 1500 47-77 / 29, 2048 60-102 / 29.
 inline bool embed_small(int64_t tokens, int64_t cols)
 {
     return tokens <= EMBED_SMALL || (tokens <= 2048 && cols <= 2048);
@@ -75,7 +78,7 @@ inline int xent_prep(int64_t tokens) { return tokens <= 32768 ? XENT_STEP : 8 * 
 // Parts that dX's sum over `cols` columns of a piece is cut into, for n rows of
 // tiles of `edge` and tiles_n columns of them: those that fill 1 to 4 rounds of
 // the chip's `slots` workgroups, or one, whichever is cheapest, a tile's way
-// costing some 600 columns besides.  Sizes are below 2^21, tiles below 2^22.
+// costing some 600 columns besides.  Sizes are below 2^21, tiles at most 2^23.
 inline __host__ __device__ int xent_splits(int n, int edge, int tiles_n, int cols, int slots, int most)
 {
     const int tiles = (n + edge - 1) / edge * tiles_n;

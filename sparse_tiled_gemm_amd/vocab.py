@@ -16,8 +16,10 @@ dX).  dE begins as zeros, so that a new object's first call may add to it.  dlos
 1 / (number of targets).
 
 All buffers are made once and belong to the object, those it returns among
-them: each is overwritten by the next call of its kind.  E is read where it
-lies, at each call.  A step only enqueues kernels, so it may be captured into a HIP
+them: each is overwritten by the next call of its kind.  (dE and the workspace of
+the gradients are there for an object that only scores too.)  One workspace serves
+all calls, so an object's calls belong on one stream at a time.  E has at most
+2^20 rows and is read where it lies, at each call.  A step only enqueues kernels, so it may be captured into a HIP
 graph; X, ids and targets must not change between a call and its gradient's.
 
 `python -m sparse_tiled_gemm_amd.vocab` runs a step and prints the time of each part.
